@@ -64,6 +64,7 @@
 #define KATA_H_
 
 #include <stddef.h>
+#include <stdint.h>
 
 #ifdef __cplusplus
 extern "C" {
@@ -399,6 +400,121 @@ kata_status kata_state_unpack(const float *state_p, const float *z_p, float *sta
 kata_status kata_decode_step_packed(const void *q, const void *k, const void *v, void *out,
                                     float *state_p, float *z_p, int B, int H, int dk, int dv,
                                     kata_dtype dtype, kata_stream_t stream);
+
+/*
+ * Queries and keys prepared for the calls above: RMS norm of every head's row,
+ * a gain per coordinate, and the rotation by position, in one pass from the
+ * projections' token-major layout into the head-major layout that the attention
+ * calls read.  (The sources name positional embeddings among what interacts with
+ * the feature geometry, arXiv abstract, and give no formula; this is the usual
+ * rotation of coordinate pairs.)  For a row x of d coordinates at position p:
+ *
+ *     u = x / sqrt(mean_i x_i^2 + eps),   z_i = weight_i u_i,
+ *     (out_a, out_b) = (z_a cos t - z_b sin t, z_a sin t + z_b cos t),
+ *     t = p * inv_freq[i]  for pair i = 0 .. n_rot - 1,
+ *
+ * with pair i = (i, i + n_rot), or (2 i, 2 i + 1) if interleaved; the coordinates
+ * from 2 n_rot on are not rotated.  The angle is formed and reduced in 64 bits.
+ *
+ *   q, k      [B, T, Hq, d], [B, T, Hk, d] dtype, any strides: element
+ *             (b, t, h, i) at b * s[0] + t * s[1] + h * s[2] + i, s = q_strides
+ *             or k_strides (in elements, >= 0; along every axis longer than 1 a
+ *             multiple of 16 bytes).  So slices of one fused projection need no
+ *             copy.  k may be NULL with Hk = 0.
+ *   q_out, k_out  [B, Hq, T, d], [B, Hk, T, d] dtype, dense
+ *   q_weight, k_weight  nullable (gain 1), [d] fp32
+ *   inv_freq  [n_rot] fp32; n_rot = 0 (inv_freq may be NULL): no rotation.
+ *             n_rot <= d / 2; not interleaved: a multiple of 4, else
+ *             KATA_ERR_UNSUPPORTED
+ *   positions nullable (t), int64: of (b, t) at b * pos_stride + t (pos_stride 0:
+ *             the same for every b).  A decode step is T = 1 with each sequence's
+ *             own position.
+ *   eps       > 0 (a row of zeros gives zeros)
+ *
+ * kata_qk_norm_rotate_backward: the gradient.  dq_out, dk_out are the gradients
+ * of q_out and k_out (dense, head-major); dq, dk receive those of q and k with
+ * strides of their own (no two rows may share memory; dq and dk may be
+ * slices of one fused buffer); dq_weight, dk_weight (nullable, fp32 [d]) those
+ * of the gains, summed over all rows in a fixed order.  The workspace is
+ * kata_qk_norm_rotate_backward_workspace_bytes(...) bytes, 256-byte aligned.
+ * dq and dk must not overlap any input.
+ *
+ * Weights, inv_freq: 16-byte aligned like every pointer; B * T * (Hq + Hk) at
+ * most 2^40.  Offsets are 64-bit.
+ */
+kata_status kata_qk_norm_rotate(const void *q, const void *k, void *q_out, void *k_out,
+                                const float *q_weight, const float *k_weight,
+                                const float *inv_freq, const int64_t *positions, int B, int T,
+                                int Hq, int Hk, int d, int n_rot, const int64_t *q_strides,
+                                const int64_t *k_strides, int64_t pos_stride, float eps,
+                                int interleaved, kata_dtype dtype, kata_stream_t stream);
+size_t kata_qk_norm_rotate_backward_workspace_bytes(int B, int T, int Hq, int Hk, int d);
+kata_status kata_qk_norm_rotate_backward(
+    const void *dq_out, const void *dk_out, const void *q, const void *k, const float *q_weight,
+    const float *k_weight, const float *inv_freq, const int64_t *positions, void *dq, void *dk,
+    float *dq_weight, float *dk_weight, int B, int T, int Hq, int Hk, int d, int n_rot,
+    const int64_t *q_strides, const int64_t *k_strides, const int64_t *dq_strides,
+    const int64_t *dk_strides, int64_t pos_stride, float eps, int interleaved, kata_dtype dtype,
+    void *workspace, size_t workspace_bytes, kata_stream_t stream);
+
+/*
+ * KATA attention to another sequence (cross attention: an encoder's states of
+ * another length).  Every query sees the first key_lengths[b] of its sequence's
+ * Tk keys, whatever its own position:
+ *
+ *     w_ts = (q_t.k_s)^2,   l_t = sum_{s < key_lengths[b]} w_ts,
+ *     y_t  = sum_{s < key_lengths[b]} w_ts v_s / l_t              (0 if l_t = 0)
+ *
+ * (the weights of this file's head with the causal mask replaced by a length;
+ * the convex output gate of summary 2.1 holds as before).
+ *
+ *   q      [B, H, Tq, d] dtype     out  [B, H, Tq, d] dtype
+ *   k, v   [B, Hkv, Tk, d] dtype; Hkv divides H, query head h uses key head
+ *          h / (H / Hkv)
+ *   key_lengths  nullable (all Tk keys), [B] int32 in device memory; values are
+ *          clamped to [0, Tk].  What k and v hold from there on is not used,
+ *          NaN included; a sequence of length 0 gives rows of zeros.
+ *   y_out  nullable, [B, H, Tq, d] fp32: the output before its rounding
+ *   den_out  nullable, [B, H, Tq] fp32: l_t
+ *          Both are what kata_cross_backward reads.
+ *   workspace  kata_cross_forward_workspace_bytes(...) bytes (may be 0), 256-byte
+ *          aligned: partial sums when few rows attend to many keys, whose keys
+ *          are then split over the SMs and joined.  A decode step is Tq = 1.
+ *
+ * KATA_BF16 runs on the tensor cores for every d (fp32 accumulation; the weights
+ * are rounded to bf16 once, in the numerator and the denominator alike),
+ * KATA_F32 in fp32 on the CUDA cores.
+ *
+ * kata_cross_backward: with dout the gradient of out and D_t = dout_t.y_t,
+ *
+ *     dq_t = sum_s c_ts k_s,  dk_s = sum_t c_ts q_t,  dv_s = sum_t (w_ts / l_t) dout_t,
+ *     c_ts = 2 (q_t.k_s) (dout_t.v_s - D_t) / l_t                  (0 if l_t = 0)
+ *
+ * dk and dv are summed over the query heads that share a key head, and are zero
+ * from key_lengths[b] on.  y and den are the forward's y_out and den_out for the
+ * same q, k, v and key_lengths (another y or den gives wrong gradients, never a
+ * fault).  No atomics: the same inputs give the same bits.
+ * Workspace: kata_cross_backward_workspace_bytes(...) bytes, 256-byte aligned.
+ *
+ * The size queries return 0 for arguments that the calls would reject.  Sizes:
+ * d in {16, 32, 64}; (H / Hkv) * Tq below 2^31 - 256 and the number of work items
+ * (256 rows, or 16 in fp32, of one key head) below 2^31, else
+ * KATA_ERR_UNSUPPORTED.
+ */
+size_t kata_cross_forward_workspace_bytes(int B, int H, int Hkv, int Tq, int Tk, int d,
+                                          kata_dtype dtype);
+kata_status kata_cross_forward(const void *q, const void *k, const void *v,
+                               const int32_t *key_lengths, void *out, int B, int H, int Hkv,
+                               int Tq, int Tk, int d, kata_dtype dtype, float *y_out,
+                               float *den_out, void *workspace, size_t workspace_bytes,
+                               kata_stream_t stream);
+size_t kata_cross_backward_workspace_bytes(int B, int H, int Hkv, int Tq, int Tk, int d,
+                                           kata_dtype dtype);
+kata_status kata_cross_backward(const void *dout, const void *q, const void *k, const void *v,
+                                const float *y, const float *den, const int32_t *key_lengths,
+                                void *dq, void *dk, void *dv, int B, int H, int Hkv, int Tq,
+                                int Tk, int d, kata_dtype dtype, void *workspace,
+                                size_t workspace_bytes, kata_stream_t stream);
 
 /*
  * Synchronises `stream`, returns and clears the device status word that

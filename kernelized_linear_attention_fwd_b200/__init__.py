@@ -13,12 +13,19 @@ from .binding import (  # noqa: F401
     kata_chunked_forward_noalloc,
     kata_chunked_forward_workspace_bytes,
     kata_chunked_state,
+    kata_cross_backward,
+    kata_cross_backward_workspace_bytes,
+    kata_cross_forward,
+    kata_cross_forward_workspace_bytes,
     kata_decode_step,
     kata_decode_step_packed,
     kata_get_device_status,
     kata_mg_chunked_forward,
     kata_mg_chunked_forward_workspace_bytes,
     kata_mg_decode_step,
+    kata_qk_norm_rotate,
+    kata_qk_norm_rotate_backward,
+    kata_qk_norm_rotate_backward_workspace_bytes,
     kata_quadratic_forward,
     kata_state_pack,
     kata_state_unpack,

@@ -43,6 +43,13 @@ EXPORTS = (
     "kata_decode_step_packed",
     "kata_state_pack",
     "kata_state_unpack",
+    "kata_qk_norm_rotate",
+    "kata_qk_norm_rotate_backward_workspace_bytes",
+    "kata_qk_norm_rotate_backward",
+    "kata_cross_forward_workspace_bytes",
+    "kata_cross_forward",
+    "kata_cross_backward_workspace_bytes",
+    "kata_cross_backward",
     "kata_get_device_status",
 )
 
@@ -106,6 +113,21 @@ def load_library(path: str = LIB_PATH):
     for name in ("kata_state_pack", "kata_state_unpack"):
         getattr(lib, name).restype = i32
         getattr(lib, name).argtypes = [fp, fp, fp, fp, i32, i32, i32, i32, vp]
+    f32, i64, i64p = ctypes.c_float, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)
+    lib.kata_qk_norm_rotate.restype = i32
+    lib.kata_qk_norm_rotate.argtypes = [vp] * 8 + [i32] * 6 + [i64p] * 2 + [i64, f32, i32, i32, vp]
+    lib.kata_qk_norm_rotate_backward_workspace_bytes.restype = sz
+    lib.kata_qk_norm_rotate_backward_workspace_bytes.argtypes = [i32] * 5
+    lib.kata_qk_norm_rotate_backward.restype = i32
+    lib.kata_qk_norm_rotate_backward.argtypes = ([vp] * 12 + [i32] * 6 + [i64p] * 4
+                                                 + [i64, f32, i32, i32, vp, sz, vp])
+    for name in ("kata_cross_forward_workspace_bytes", "kata_cross_backward_workspace_bytes"):
+        getattr(lib, name).restype = sz
+        getattr(lib, name).argtypes = [i32] * 7
+    lib.kata_cross_forward.restype = i32
+    lib.kata_cross_forward.argtypes = [vp] * 5 + [i32] * 7 + [fp, fp, vp, sz, vp]
+    lib.kata_cross_backward.restype = i32
+    lib.kata_cross_backward.argtypes = [vp] * 10 + [i32] * 7 + [vp, sz, vp]
     lib.kata_get_device_status.restype = i32
     lib.kata_get_device_status.argtypes = [vp]
     _lib = lib
@@ -613,6 +635,263 @@ def kata_state_unpack(state_p, z_p, state=None, z=None, stream=None):
     if st != KATA_OK:
         raise KataError(st, "kata_state_unpack")
     return state, z
+
+
+def _new(stream, shape, dtype, device):
+    """Tensor for a call on `stream` (None: the current one), from that stream's
+    memory: a block that the current stream has just let go may still be in use
+    there."""
+    import torch
+
+    if stream is None or stream.device != device:  # another device's stream is refused later
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _token_major(t, name, heads=None, like=None):
+    """t is a CUDA [B, T, H, d] tensor with a contiguous last axis (any other
+    strides), matching `like` in B, T, d, dtype and device when given."""
+    if not t.is_cuda:
+        raise KataError(KATA_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
+    if t.dim() != 4:
+        raise KataError(KATA_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, want [B, T, H, d]")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise KataError(KATA_ERR_INVALID_ARG, f"the last axis of {name} must be contiguous")
+    if like is not None:
+        B, T, H, d = like.shape
+        want = (B, T, t.shape[2] if heads is None else heads, d)
+        if tuple(t.shape) != want:
+            raise KataError(KATA_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, want {want}")
+        if t.dtype != like.dtype:
+            raise KataError(KATA_ERR_INVALID_ARG, f"{name} has dtype {t.dtype}, want {like.dtype}")
+        if t.device != like.device:
+            raise KataError(KATA_ERR_INVALID_ARG, f"{name} is on {t.device}, want {like.device}")
+
+
+def _strides(t):
+    return None if t is None else (ctypes.c_int64 * 3)(*t.stride()[:3])
+
+
+def _norm_inputs(q, k, q_weight, k_weight, inv_freq, positions):
+    """Checks shared by both directions; (B, T, Hq, Hk, d, n_rot, positions' row stride)."""
+    import torch
+
+    _token_major(q, "q")
+    B, T, Hq, d = q.shape
+    dev = q.device
+    Hk = 0
+    if k is not None:
+        _token_major(k, "k", like=q)
+        Hk = k.shape[2]
+    elif k_weight is not None:
+        raise KataError(KATA_ERR_INVALID_ARG, "k_weight without k")
+    _check(q_weight, "q_weight", (d,), torch.float32, device=dev)
+    _check(k_weight, "k_weight", (d,), torch.float32, device=dev)
+    n_rot = 0
+    if inv_freq is not None:
+        n_rot = inv_freq.numel()
+        _check(inv_freq, "inv_freq", (n_rot,), torch.float32, device=dev)
+    pos_stride = 0
+    if positions is not None:
+        if not positions.is_cuda or positions.device != dev:
+            raise KataError(KATA_ERR_INVALID_ARG, f"positions must be on {dev}")
+        if positions.dtype != torch.int64:
+            raise KataError(KATA_ERR_INVALID_ARG, f"positions has dtype {positions.dtype}, want {torch.int64}")
+        if tuple(positions.shape) not in ((T,), (B, T)):
+            raise KataError(KATA_ERR_INVALID_ARG,
+                            f"positions has shape {tuple(positions.shape)}, want {(T,)} or {(B, T)}")
+        if T > 1 and positions.stride(-1) != 1:
+            raise KataError(KATA_ERR_INVALID_ARG, "the last axis of positions must be contiguous")
+        pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    return B, T, Hq, Hk, d, n_rot, pos_stride
+
+
+def kata_qk_norm_rotate(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positions=None,
+                        eps=1e-6, interleaved=False, q_out=None, k_out=None, stream=None):
+    """(q_out [B,Hq,T,d], k_out [B,Hk,T,d] or None): per-head RMS norm of q
+    [B,T,Hq,d] and k [B,T,Hk,d] (token-major, any strides: slices of a fused
+    projection), times the fp32 gains q_weight, k_weight [d] (None: 1), rotated
+    by position * inv_freq [n_rot] fp32 (None: no rotation).  positions: int64
+    [B,T] or [T] (None: 0 .. T-1).  interleaved: pairs (2i, 2i+1) instead of
+    (i, i + n_rot)."""
+    import torch
+
+    lib = load_library()
+    B, T, Hq, Hk, d, n_rot, pos_stride = _norm_inputs(q, k, q_weight, k_weight, inv_freq, positions)
+    dev = q.device
+    code = _dtype_code(q)
+    if q_out is None:
+        q_out = _new(stream, (B, Hq, T, d), q.dtype, dev)
+    _check(q_out, "q_out", (B, Hq, T, d), q.dtype, device=dev)
+    if k is None:
+        if k_out is not None:
+            raise KataError(KATA_ERR_INVALID_ARG, "k_out without k")
+    elif k_out is None:
+        k_out = _new(stream, (B, Hk, T, d), q.dtype, dev)
+    _check(k_out, "k_out", (B, Hk, T, d), q.dtype, device=dev)
+    with _on_device(dev):
+        st = lib.kata_qk_norm_rotate(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(q_weight),
+                                     _ptr(k_weight), _ptr(inv_freq) if n_rot else None,
+                                     _ptr(positions), B, T, Hq, Hk, d, n_rot, _strides(q),
+                                     _strides(k), pos_stride, float(eps), int(bool(interleaved)),
+                                     code, _stream_handle(stream, dev))
+    if st != KATA_OK:
+        raise KataError(st, "kata_qk_norm_rotate")
+    return q_out, k_out
+
+
+def kata_qk_norm_rotate_backward_workspace_bytes(B, T, Hq, Hk, d) -> int:
+    return int(load_library().kata_qk_norm_rotate_backward_workspace_bytes(B, T, Hq, Hk, d))
+
+
+def kata_qk_norm_rotate_backward(dq_out, dk_out, q, k=None, q_weight=None, k_weight=None,
+                                 inv_freq=None, positions=None, eps=1e-6, interleaved=False,
+                                 dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None,
+                                 stream=None):
+    """(dq, dk, dq_weight, dk_weight): the gradient of kata_qk_norm_rotate, from
+    those of its outputs (dq_out [B,Hq,T,d], dk_out [B,Hk,T,d]) and its inputs.
+    dq, dk are [B,T,H,d] with strides of their own (dense if allocated here; they
+    may be slices of one fused gradient); the gains' gradients are fp32 [d].
+    Without k, dk and dk_weight are None."""
+    import torch
+
+    lib = load_library()
+    B, T, Hq, Hk, d, n_rot, pos_stride = _norm_inputs(q, k, q_weight, k_weight, inv_freq, positions)
+    dev = q.device
+    code = _dtype_code(q)
+    _check(dq_out, "dq_out", (B, Hq, T, d), q.dtype, device=dev)
+    if k is None:
+        for t, name in ((dk_out, "dk_out"), (dk, "dk"), (dk_weight, "dk_weight")):
+            if t is not None:
+                raise KataError(KATA_ERR_INVALID_ARG, f"{name} without k")
+    else:
+        _check(dk_out, "dk_out", (B, Hk, T, d), q.dtype, device=dev)
+        if dk is None:
+            dk = _new(stream, (B, T, Hk, d), q.dtype, dev)
+        if dk_weight is None:
+            dk_weight = _new(stream, (d,), torch.float32, dev)
+        _token_major(dk, "dk", heads=Hk, like=q)
+    if dq is None:
+        dq = _new(stream, (B, T, Hq, d), q.dtype, dev)
+    if dq_weight is None:
+        dq_weight = _new(stream, (d,), torch.float32, dev)
+    _token_major(dq, "dq", heads=Hq, like=q)
+    _check(dq_weight, "dq_weight", (d,), torch.float32, device=dev)
+    _check(dk_weight, "dk_weight", (d,), torch.float32, device=dev)
+    need = lib.kata_qk_norm_rotate_backward_workspace_bytes(B, T, Hq, Hk, d)
+    workspace, nbytes = _sized_workspace(workspace, need, dev, stream)
+    with _on_device(dev):
+        st = lib.kata_qk_norm_rotate_backward(
+            _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
+            _ptr(inv_freq) if n_rot else None, _ptr(positions), _ptr(dq), _ptr(dk),
+            _ptr(dq_weight), _ptr(dk_weight), B, T, Hq, Hk, d, n_rot, _strides(q), _strides(k),
+            _strides(dq), _strides(dk), pos_stride, float(eps), int(bool(interleaved)), code,
+            _ptr(workspace), nbytes, _stream_handle(stream, dev))
+    if st != KATA_OK:
+        raise KataError(st, "kata_qk_norm_rotate_backward")
+    return dq, dk, dq_weight, dk_weight
+
+
+def _sized_workspace(workspace, need, device, stream):
+    """(workspace, bytes): the caller's (on `device`) or `need` bytes allocated here."""
+    import torch
+
+    if workspace is None and need > 0:
+        workspace = _new(stream, (need,), torch.uint8, device)
+    if workspace is not None and (not workspace.is_cuda or workspace.device != device):
+        raise KataError(KATA_ERR_INVALID_ARG, f"workspace must be on {device}")
+    if workspace is not None and not workspace.is_contiguous():
+        raise KataError(KATA_ERR_INVALID_ARG, "workspace must be contiguous")
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _cross_inputs(q, k, v, key_lengths):
+    """Checks shared by both directions; (B, H, Hkv, Tq, Tk, d)."""
+    import torch
+
+    for t, name in ((q, "q"), (k, "k")):
+        if t.dim() != 4:
+            raise KataError(KATA_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, want [B, H, T, d]")
+    B, H, Tq, d = q.shape
+    Hkv, Tk = k.shape[1], k.shape[2]
+    dev = q.device
+    _check(q, "q", (B, H, Tq, d), device=dev)
+    _check(k, "k", (B, Hkv, Tk, d), q.dtype, device=dev)
+    _check(v, "v", (B, Hkv, Tk, d), q.dtype, device=dev)
+    _check(key_lengths, "key_lengths", (B,), torch.int32, device=dev)
+    return B, H, Hkv, Tq, Tk, d
+
+
+def kata_cross_forward_workspace_bytes(B, H, Hkv, Tq, Tk, d, dtype_code) -> int:
+    return int(load_library().kata_cross_forward_workspace_bytes(B, H, Hkv, Tq, Tk, d, dtype_code))
+
+
+def kata_cross_forward(q, k, v, key_lengths=None, out=None, y_out=None, den_out=None,
+                       workspace=None, stream=None):
+    """out [B,H,Tq,d]: KATA attention of q [B,H,Tq,d] to the first key_lengths[b]
+    (int32 [B]; None: all) of the keys k, v [B,Hkv,Tk,d] of another sequence;
+    Hkv divides H.  Rows without weight are zero.  y_out [B,H,Tq,d] and den_out
+    [B,H,Tq] (optional, fp32) receive the unrounded output and the summed
+    weights, which kata_cross_backward reads."""
+    import torch
+
+    lib = load_library()
+    B, H, Hkv, Tq, Tk, d = _cross_inputs(q, k, v, key_lengths)
+    dev = q.device
+    code = _dtype_code(q)
+    if out is None:
+        out = _new(stream, (B, H, Tq, d), q.dtype, dev)
+    _check(out, "out", (B, H, Tq, d), q.dtype, device=dev)
+    _check(y_out, "y_out", (B, H, Tq, d), torch.float32, device=dev)
+    _check(den_out, "den_out", (B, H, Tq), torch.float32, device=dev)
+    need = lib.kata_cross_forward_workspace_bytes(B, H, Hkv, Tq, Tk, d, code)
+    workspace, nbytes = _sized_workspace(workspace, need, dev, stream)
+    with _on_device(dev):
+        st = lib.kata_cross_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(key_lengths), _ptr(out), B, H,
+                                    Hkv, Tq, Tk, d, code, _ptr(y_out), _ptr(den_out),
+                                    _ptr(workspace), nbytes, _stream_handle(stream, dev))
+    if st != KATA_OK:
+        raise KataError(st, "kata_cross_forward")
+    return out
+
+
+def kata_cross_backward_workspace_bytes(B, H, Hkv, Tq, Tk, d, dtype_code) -> int:
+    return int(load_library().kata_cross_backward_workspace_bytes(B, H, Hkv, Tq, Tk, d, dtype_code))
+
+
+def kata_cross_backward(dout, q, k, v, y, den, key_lengths=None, dq=None, dk=None, dv=None,
+                        workspace=None, stream=None):
+    """(dq, dk, dv): the gradient of kata_cross_forward, from that of its output
+    and what it wrote to y_out and den_out for the same q, k, v, key_lengths."""
+    import torch
+
+    lib = load_library()
+    B, H, Hkv, Tq, Tk, d = _cross_inputs(q, k, v, key_lengths)
+    dev = q.device
+    code = _dtype_code(q)
+    _check(dout, "dout", (B, H, Tq, d), q.dtype, device=dev)
+    _check(y, "y", (B, H, Tq, d), torch.float32, device=dev)
+    _check(den, "den", (B, H, Tq), torch.float32, device=dev)
+    if dq is None:
+        dq = _new(stream, (B, H, Tq, d), q.dtype, dev)
+    if dk is None:
+        dk = _new(stream, (B, Hkv, Tk, d), q.dtype, dev)
+    if dv is None:
+        dv = _new(stream, (B, Hkv, Tk, d), q.dtype, dev)
+    _check(dq, "dq", (B, H, Tq, d), q.dtype, device=dev)
+    _check(dk, "dk", (B, Hkv, Tk, d), q.dtype, device=dev)
+    _check(dv, "dv", (B, Hkv, Tk, d), q.dtype, device=dev)
+    need = lib.kata_cross_backward_workspace_bytes(B, H, Hkv, Tq, Tk, d, code)
+    workspace, nbytes = _sized_workspace(workspace, need, dev, stream)
+    with _on_device(dev):
+        st = lib.kata_cross_backward(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(y), _ptr(den),
+                                     _ptr(key_lengths), _ptr(dq), _ptr(dk), _ptr(dv), B, H, Hkv,
+                                     Tq, Tk, d, code, _ptr(workspace), nbytes,
+                                     _stream_handle(stream, dev))
+    if st != KATA_OK:
+        raise KataError(st, "kata_cross_backward")
+    return dq, dk, dv
 
 
 def kata_get_device_status(stream=None) -> int:

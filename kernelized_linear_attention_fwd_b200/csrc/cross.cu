@@ -1,0 +1,181 @@
+// Cross attention: the steps around the main kernels (cross_tc.cu, cross_simt.cu)
+// that both types share: the backward pass's row statistics, and the joins of
+// partial sums when a long axis was split over several CTAs.
+#include <cuda_bf16.h>
+
+#include "kata_internal.cuh"
+
+namespace kata {
+namespace {
+
+// Row statistics of the backward pass: delta = dy.y (y the forward's unrounded
+// output) and 1 / den (0 for a row without weight), zeros in the padding up to
+// R_pad.  8 lanes per row.
+template <typename T>
+__global__ void __launch_bounds__(256)
+cross_stats_kernel(const T *dout, const float *y, const float *den, float *delta, float *rden, long long BH, int R,
+                   int R_pad, int d) {
+    const long long n = BH * R_pad;
+    const int sub = threadIdx.x % 8;
+    for (long long x = ((long long)blockIdx.x * 256 + threadIdx.x) / 8; x < n; x += (long long)gridDim.x * 32) {
+        const long long bh = x / R_pad;
+        const int r = (int)(x - bh * R_pad);
+        float s = 0.f, rd = 0.f;
+        if (r < R) {
+            const long long row = bh * R + r;
+            for (int c = 4 * sub; c < d; c += 32) {
+                const float4 v = *reinterpret_cast<const float4 *>(y + row * d + c);
+                s = fmaf(load_f32(dout, row * d + c), v.x, s);
+                s = fmaf(load_f32(dout, row * d + c + 1), v.y, s);
+                s = fmaf(load_f32(dout, row * d + c + 2), v.z, s);
+                s = fmaf(load_f32(dout, row * d + c + 3), v.w, s);
+            }
+            rd = cross_recip(den[row]);
+        }
+        // the 8 lanes of a row run the loop together
+        const unsigned mask = 0xffu << (threadIdx.x % 32 / 8 * 8);
+        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(mask, s, o);
+        if (sub == 0) {
+            delta[x] = s;
+            rden[x] = rd;
+        }
+    }
+}
+
+// Joins the pieces of a row: sum over splits in order, by G groups of 16 threads
+// each (thread = 4 columns), then the groups in order.  kJoinDen: divided by the
+// summed denominators (forward; y and den exported if given); kJoinRow: times
+// 2 / l of the row (dq); kJoinPlain: as is (dk, dv).
+enum Join { kJoinDen, kJoinRow, kJoinPlain };
+template <typename T, int JOIN, int G>
+__global__ void __launch_bounds__(256)
+cross_join_kernel(const float *part, const float *part_l, const float *rden, T *out, float *y, float *den,
+                  long long n_rows, long long split_stride, int splits, int R, int R_pad, int d) {
+    constexpr int kRows = 16 / G;
+    __shared__ float4 red[16][16];
+    __shared__ float red_l[16];
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, g = ty % G, c = 4 * tx;
+    const long long row = (long long)blockIdx.x * kRows + ty / G;
+    const bool on = row < n_rows;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    if (on && c < d) {
+#pragma unroll 4
+        for (int x = g; x < splits; x += G) {
+            const float4 v = *reinterpret_cast<const float4 *>(part + (x * split_stride + row) * d + c);
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+            if (JOIN == kJoinDen) l += part_l[x * split_stride + row];
+        }
+    }
+    if (G > 1) {
+        red[ty][tx] = s;
+        if (JOIN == kJoinDen && tx == 0) red_l[ty] = l;
+        __syncthreads();
+        if (g > 0) return;
+        s = red[ty][tx];
+        l = JOIN == kJoinDen ? red_l[ty] : 0.f;
+        for (int x = 1; x < G; ++x) {
+            const float4 v = red[ty + x][tx];
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+            if (JOIN == kJoinDen) l += red_l[ty + x];
+        }
+    }
+    if (!on || c >= d) return;
+    float f = 1.f;
+    if (JOIN == kJoinDen) f = cross_recip(l);
+    if (JOIN == kJoinRow) f = 2.f * rden[row / R * R_pad + row % R];
+    s.x *= f;
+    s.y *= f;
+    s.z *= f;
+    s.w *= f;
+    const long long o = row * d + c;
+    store_out(out, o, s.x);
+    store_out(out, o + 1, s.y);
+    store_out(out, o + 2, s.z);
+    store_out(out, o + 3, s.w);
+    if (JOIN == kJoinDen) {
+        if (y) *reinterpret_cast<float4 *>(y + o) = s;
+        if (den && c == 0) den[row] = l;
+    }
+}
+
+template <typename T, int JOIN>
+cudaError_t launch_join(const CrossPlan &p, CrossMode mode, const float *part, const float *part_l,
+                        const float *rden, void *out, float *y, float *den, long long n_rows,
+                        long long split_stride, cudaStream_t st) {
+    const int s = p.splits[mode];
+    ProfScope prof("cross_join", st);
+    if (s > 8)
+        cross_join_kernel<T, JOIN, 16><<<(unsigned)n_rows, 256, 0, st>>>(
+            part, part_l, rden, static_cast<T *>(out), y, den, n_rows, split_stride, s, p.R, p.R_pad, p.d);
+    else
+        cross_join_kernel<T, JOIN, 1><<<(unsigned)((n_rows + 15) / 16), 256, 0, st>>>(
+            part, part_l, rden, static_cast<T *>(out), y, den, n_rows, split_stride, s, p.R, p.R_pad, p.d);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_main(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    return p.dtype == KATA_BF16 ? launch_cross_tc(mode, p, io, st) : launch_cross_simt(mode, p, io, st);
+}
+
+template <typename T>
+cudaError_t forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    cudaError_t e = launch_main(kCrossFwd, p, io, st);
+    if (e != cudaSuccess || p.splits[kCrossFwd] == 1) return e;
+    const char *ws = static_cast<const char *>(io.ws);
+    return launch_join<T, kJoinDen>(p, kCrossFwd, reinterpret_cast<const float *>(ws + p.ws_part[kCrossFwd]),
+                                    reinterpret_cast<const float *>(ws + p.ws_part_l), nullptr, io.out, io.y, io.den,
+                                    p.BH * p.R, p.BH * p.R, st);
+}
+
+template <typename T>
+cudaError_t backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    char *ws = static_cast<char *>(io.ws);
+    float *delta = reinterpret_cast<float *>(ws + p.ws_delta), *rden = reinterpret_cast<float *>(ws + p.ws_rden);
+    {
+        ProfScope prof("cross_stats", st);
+        const long long blocks = (p.BH * p.R_pad + 31) / 32, most = 8LL * kPlanSms;
+        cross_stats_kernel<T><<<(unsigned)(blocks < most ? blocks : most), 256, 0, st>>>(
+            static_cast<const T *>(io.dout), io.y, io.den, delta, rden, p.BH, p.R, p.R_pad, p.d);
+    }
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if ((e = launch_main(kCrossDq, p, io, st)) != cudaSuccess) return e;
+    if (p.splits[kCrossDq] > 1) {
+        e = launch_join<T, kJoinRow>(p, kCrossDq, reinterpret_cast<const float *>(ws + p.ws_part[kCrossDq]), nullptr,
+                                     rden, io.dq, nullptr, nullptr, p.BH * p.R, p.BH * p.R, st);
+        if (e != cudaSuccess) return e;
+    }
+    if ((e = launch_main(kCrossDkv, p, io, st)) != cudaSuccess) return e;
+    if (p.splits[kCrossDkv] > 1) {
+        const float *part = reinterpret_cast<const float *>(ws + p.ws_part[kCrossDkv]);
+        const long long n = p.BH * p.Tk;
+        e = launch_join<T, kJoinPlain>(p, kCrossDkv, part, nullptr, nullptr, io.dv, nullptr, nullptr, n, 2 * n, st);
+        if (e != cudaSuccess) return e;
+        e = launch_join<T, kJoinPlain>(p, kCrossDkv, part + n * p.d, nullptr, nullptr, io.dk, nullptr, nullptr, n,
+                                       2 * n, st);
+    }
+    return e;
+}
+
+}  // namespace
+
+CrossTile cross_tile(CrossMode mode, const CrossPlan &p) {
+    if (p.dtype == KATA_BF16) return {256, mode == kCrossFwd ? 128 : 64};
+    return {mode == kCrossFwd && p.R <= 16 ? 16 : 64, 64};
+}
+
+cudaError_t launch_cross_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    return p.dtype == KATA_BF16 ? forward<__nv_bfloat16>(p, io, st) : forward<float>(p, io, st);
+}
+cudaError_t launch_cross_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    return p.dtype == KATA_BF16 ? backward<__nv_bfloat16>(p, io, st) : backward<float>(p, io, st);
+}
+
+}  // namespace kata

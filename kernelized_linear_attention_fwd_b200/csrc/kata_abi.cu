@@ -13,21 +13,9 @@ namespace {
 
 __device__ int g_device_status = 0;
 
-
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 bool valid_chunk(int C) {
     return C == 16 || C == 32 || C == 64 || C == 128 || C == 256 || C == 512 || C == 1024 ||
            C == 2048 || C == 4096;
-}
-
-bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
 }
 
 // Segment length: states are stored every L tokens.  Inside a segment the

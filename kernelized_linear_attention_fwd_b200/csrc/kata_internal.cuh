@@ -100,6 +100,14 @@ kata_status make_quadratic_plan(int B, int H, int T, int dk, int dv, kata_dtype 
 // fails (one per device; resolved on first use with that device current).
 int *device_status_ptr();
 
+// Argument checks shared by the entry points.
+inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
 // True when every non-null pointer is memory of the current device (or
 // managed memory).  Host memory and another device's memory are rejected, so
 // a call given them returns an error instead of launching kernels that would
@@ -174,6 +182,78 @@ cudaError_t launch_tc_forward(const Plan &p, const void *q, const void *k, const
 // Streaming multiprocessors of the current device (cached).
 int num_sms();
 }  // namespace tc
+
+// Streaming multiprocessors that launch and workspace plans are made for: a
+// constant, so that a workspace's size depends on the call's arguments only.
+constexpr int kPlanSms = 148;
+
+// Head norm with rotation (norm_rotate.cu); index 0 the queries, 1 the keys
+// (H[1] = 0: no keys).
+struct NormRotate {
+    bool backward = false, interleaved = false;
+    int B, T, d, n_rot;
+    int H[2];
+    kata_dtype dtype;
+    float eps;
+    const void *x[2];
+    long long xs[2][3];  // strides of batch, token, head (elements)
+    void *y[2];
+    const float *w[2];
+    const float *inv_freq;
+    const long long *positions;
+    long long pos_stride;
+    const void *gy[2];
+    void *dx[2];
+    long long ds[2][3];
+    float *dw[2];
+    void *ws;  // backward: grid blocks x 2 d floats
+};
+dim3 norm_rotate_grid(const NormRotate &p);
+cudaError_t launch_norm_rotate(const NormRotate &p, cudaStream_t st);
+
+// Cross attention (cross_tc.cu for bf16, cross_simt.cu for fp32).  The query
+// heads that share a key head are consecutive in memory, so they are the rows of
+// one problem: BH = B Hkv problems of R = (H / Hkv) Tq rows and Tk keys.
+enum CrossMode : int { kCrossFwd = 0, kCrossDq = 1, kCrossDkv = 2 };
+struct CrossPlan {
+    int B, H, Hkv, Tq, Tk, d;
+    kata_dtype dtype;
+    long long BH;
+    int R;             // rows per problem
+    int R_pad;         // R rounded up to 64: row stride of the statistics
+    int splits[3];     // per CrossMode: pieces of the summed axis (1: no join)
+    // workspace (bytes)
+    size_t ws_part[3];  // partial sums of each mode
+    size_t ws_part_l;   // forward: partial denominators
+    size_t ws_delta;    // backward: [BH][R_pad] dy.y, then [BH][R_pad] 1 / den
+    size_t ws_rden;
+    size_t ws_fwd_bytes, ws_bwd_bytes;
+};
+struct CrossIo {
+    const void *q, *k, *v, *dout;
+    const int *key_lengths;  // [B] or null
+    void *out;
+    float *y, *den;          // forward: nullable exports; backward: inputs
+    void *dq, *dk, *dv;
+    void *ws;
+};
+cudaError_t launch_cross_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
+cudaError_t launch_cross_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
+// One mode's main kernel: bf16 on the tensor cores, fp32 on the CUDA cores.
+cudaError_t launch_cross_tc(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
+cudaError_t launch_cross_simt(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
+// Row and column extents of a mode's work: rows per item and columns per step.
+struct CrossTile {
+    int rows, cols;
+};
+CrossTile cross_tile(CrossMode mode, const CrossPlan &p);
+
+// Keys that sequence b may attend to: its length, within [0, Tk].
+__device__ __forceinline__ int cross_length(const int *key_lengths, int b, int Tk) {
+    return key_lengths ? min(max(__ldg(key_lengths + b), 0), Tk) : Tk;
+}
+// 1 / den, and 0 for a row without weight.
+__device__ __forceinline__ float cross_recip(float den) { return den == 0.f ? 0.f : 1.f / den; }
 
 // Decode step on the dense (d^2 rows) or packed (d(d+1)/2 rows) state layout.
 cudaError_t launch_decode(int B, int H, int dk, int dv, kata_dtype dtype, const void *q,
