@@ -637,16 +637,50 @@ def kata_state_unpack(state_p, z_p, state=None, z=None, stream=None):
     return state, z
 
 
-def _new(stream, shape, dtype, device):
-    """Tensor for a call on `stream` (None: the current one), from that stream's
-    memory: a block that the current stream has just let go may still be in use
-    there."""
+# The calls below are short next to Python's share of them (a decode step's
+# kernels take 3 to 5 us), so their checks are one expression per tensor, with the
+# message worked out only on failure, and the device is switched only if needed.
+_I64x3 = ctypes.c_int64 * 3
+
+
+def _is(t, name, shape, dtype, device):
+    """`t` is a contiguous tensor of `shape`, `dtype` on the CUDA device `device`."""
+    if not (t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()):
+        _check(t, name, shape, dtype, device)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _run(name, device, stream, *args):
+    """Calls the C function `name`(*args, stream) with `device` current."""
     import torch
 
-    if stream is None or stream.device != device:  # another device's stream is refused later
-        return torch.empty(shape, dtype=dtype, device=device)
+    fn = getattr(load_library(), name)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        handle = _stream_handle(stream, device)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, handle)
+    else:
+        with _on_device(device):
+            st = fn(*args, handle)
+    if st != KATA_OK:
+        raise KataError(st, name)
+
+
+def _new(stream, like, shape, dtype=None):
+    """Tensor for a call on `stream` (None: the current one), on the device of
+    `like`, from that stream's memory: a block that the current stream has just
+    let go may still be in use there."""
+    import torch
+
+    if stream is None or stream.device != like.device:  # another device's stream is refused later
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _token_major(t, name, heads=None, like=None):
@@ -670,7 +704,10 @@ def _token_major(t, name, heads=None, like=None):
 
 
 def _strides(t):
-    return None if t is None else (ctypes.c_int64 * 3)(*t.stride()[:3])
+    if t is None:
+        return None
+    s = t.stride()
+    return _I64x3(s[0], s[1], s[2])
 
 
 def _norm_inputs(q, k, q_weight, k_weight, inv_freq, positions):
@@ -686,19 +723,21 @@ def _norm_inputs(q, k, q_weight, k_weight, inv_freq, positions):
         Hk = k.shape[2]
     elif k_weight is not None:
         raise KataError(KATA_ERR_INVALID_ARG, "k_weight without k")
-    _check(q_weight, "q_weight", (d,), torch.float32, device=dev)
-    _check(k_weight, "k_weight", (d,), torch.float32, device=dev)
+    if q_weight is not None:
+        _is(q_weight, "q_weight", (d,), torch.float32, dev)
+    if k_weight is not None:
+        _is(k_weight, "k_weight", (d,), torch.float32, dev)
     n_rot = 0
     if inv_freq is not None:
         n_rot = inv_freq.numel()
-        _check(inv_freq, "inv_freq", (n_rot,), torch.float32, device=dev)
+        _is(inv_freq, "inv_freq", (n_rot,), torch.float32, dev)
     pos_stride = 0
     if positions is not None:
-        if not positions.is_cuda or positions.device != dev:
+        if positions.device != dev:
             raise KataError(KATA_ERR_INVALID_ARG, f"positions must be on {dev}")
-        if positions.dtype != torch.int64:
+        if positions.dtype is not torch.int64:
             raise KataError(KATA_ERR_INVALID_ARG, f"positions has dtype {positions.dtype}, want {torch.int64}")
-        if tuple(positions.shape) not in ((T,), (B, T)):
+        if positions.shape != (B, T) and positions.shape != (T,):
             raise KataError(KATA_ERR_INVALID_ARG,
                             f"positions has shape {tuple(positions.shape)}, want {(T,)} or {(B, T)}")
         if T > 1 and positions.stride(-1) != 1:
@@ -715,29 +754,23 @@ def kata_qk_norm_rotate(q, k=None, q_weight=None, k_weight=None, inv_freq=None, 
     by position * inv_freq [n_rot] fp32 (None: no rotation).  positions: int64
     [B,T] or [T] (None: 0 .. T-1).  interleaved: pairs (2i, 2i+1) instead of
     (i, i + n_rot)."""
-    import torch
-
-    lib = load_library()
     B, T, Hq, Hk, d, n_rot, pos_stride = _norm_inputs(q, k, q_weight, k_weight, inv_freq, positions)
     dev = q.device
     code = _dtype_code(q)
     if q_out is None:
-        q_out = _new(stream, (B, Hq, T, d), q.dtype, dev)
-    _check(q_out, "q_out", (B, Hq, T, d), q.dtype, device=dev)
+        q_out = _new(stream, q, (B, Hq, T, d))
+    else:
+        _is(q_out, "q_out", (B, Hq, T, d), q.dtype, dev)
     if k is None:
         if k_out is not None:
             raise KataError(KATA_ERR_INVALID_ARG, "k_out without k")
     elif k_out is None:
-        k_out = _new(stream, (B, Hk, T, d), q.dtype, dev)
-    _check(k_out, "k_out", (B, Hk, T, d), q.dtype, device=dev)
-    with _on_device(dev):
-        st = lib.kata_qk_norm_rotate(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(q_weight),
-                                     _ptr(k_weight), _ptr(inv_freq) if n_rot else None,
-                                     _ptr(positions), B, T, Hq, Hk, d, n_rot, _strides(q),
-                                     _strides(k), pos_stride, float(eps), int(bool(interleaved)),
-                                     code, _stream_handle(stream, dev))
-    if st != KATA_OK:
-        raise KataError(st, "kata_qk_norm_rotate")
+        k_out = _new(stream, q, (B, Hk, T, d))
+    else:
+        _is(k_out, "k_out", (B, Hk, T, d), q.dtype, dev)
+    _run("kata_qk_norm_rotate", dev, stream, q.data_ptr(), _address(k), q_out.data_ptr(), _address(k_out),
+         _address(q_weight), _address(k_weight), _address(inv_freq) if n_rot else None, _address(positions),
+         B, T, Hq, Hk, d, n_rot, _strides(q), _strides(k), pos_stride, eps, 1 if interleaved else 0, code)
     return q_out, k_out
 
 
@@ -756,70 +789,74 @@ def kata_qk_norm_rotate_backward(dq_out, dk_out, q, k=None, q_weight=None, k_wei
     Without k, dk and dk_weight are None."""
     import torch
 
-    lib = load_library()
     B, T, Hq, Hk, d, n_rot, pos_stride = _norm_inputs(q, k, q_weight, k_weight, inv_freq, positions)
     dev = q.device
     code = _dtype_code(q)
-    _check(dq_out, "dq_out", (B, Hq, T, d), q.dtype, device=dev)
+    _is(dq_out, "dq_out", (B, Hq, T, d), q.dtype, dev)
     if k is None:
         for t, name in ((dk_out, "dk_out"), (dk, "dk"), (dk_weight, "dk_weight")):
             if t is not None:
                 raise KataError(KATA_ERR_INVALID_ARG, f"{name} without k")
     else:
-        _check(dk_out, "dk_out", (B, Hk, T, d), q.dtype, device=dev)
+        if dk_out is None:
+            raise KataError(KATA_ERR_INVALID_ARG, "k without dk_out")
+        _is(dk_out, "dk_out", (B, Hk, T, d), q.dtype, dev)
         if dk is None:
-            dk = _new(stream, (B, T, Hk, d), q.dtype, dev)
+            dk = _new(stream, q, (B, T, Hk, d))
+        else:
+            _token_major(dk, "dk", heads=Hk, like=q)
         if dk_weight is None:
-            dk_weight = _new(stream, (d,), torch.float32, dev)
-        _token_major(dk, "dk", heads=Hk, like=q)
+            dk_weight = _new(stream, q, (d,), torch.float32)
+        else:
+            _is(dk_weight, "dk_weight", (d,), torch.float32, dev)
     if dq is None:
-        dq = _new(stream, (B, T, Hq, d), q.dtype, dev)
+        dq = _new(stream, q, (B, T, Hq, d))
+    else:
+        _token_major(dq, "dq", heads=Hq, like=q)
     if dq_weight is None:
-        dq_weight = _new(stream, (d,), torch.float32, dev)
-    _token_major(dq, "dq", heads=Hq, like=q)
-    _check(dq_weight, "dq_weight", (d,), torch.float32, device=dev)
-    _check(dk_weight, "dk_weight", (d,), torch.float32, device=dev)
-    need = lib.kata_qk_norm_rotate_backward_workspace_bytes(B, T, Hq, Hk, d)
-    workspace, nbytes = _sized_workspace(workspace, need, dev, stream)
-    with _on_device(dev):
-        st = lib.kata_qk_norm_rotate_backward(
-            _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
-            _ptr(inv_freq) if n_rot else None, _ptr(positions), _ptr(dq), _ptr(dk),
-            _ptr(dq_weight), _ptr(dk_weight), B, T, Hq, Hk, d, n_rot, _strides(q), _strides(k),
-            _strides(dq), _strides(dk), pos_stride, float(eps), int(bool(interleaved)), code,
-            _ptr(workspace), nbytes, _stream_handle(stream, dev))
-    if st != KATA_OK:
-        raise KataError(st, "kata_qk_norm_rotate_backward")
+        dq_weight = _new(stream, q, (d,), torch.float32)
+    else:
+        _is(dq_weight, "dq_weight", (d,), torch.float32, dev)
+    need = load_library().kata_qk_norm_rotate_backward_workspace_bytes(B, T, Hq, Hk, d)
+    workspace, nbytes = _sized_workspace(workspace, need, q, stream)
+    _run("kata_qk_norm_rotate_backward", dev, stream, dq_out.data_ptr(), _address(dk_out), q.data_ptr(),
+         _address(k), _address(q_weight), _address(k_weight), _address(inv_freq) if n_rot else None,
+         _address(positions), dq.data_ptr(), _address(dk), dq_weight.data_ptr(), _address(dk_weight),
+         B, T, Hq, Hk, d, n_rot, _strides(q), _strides(k), _strides(dq), _strides(dk), pos_stride, eps,
+         1 if interleaved else 0, code, _address(workspace), nbytes)
     return dq, dk, dq_weight, dk_weight
 
 
-def _sized_workspace(workspace, need, device, stream):
-    """(workspace, bytes): the caller's (on `device`) or `need` bytes allocated here."""
+def _sized_workspace(workspace, need, like, stream):
+    """(workspace, bytes): the caller's (on the device of `like`) or `need` bytes allocated here."""
     import torch
 
-    if workspace is None and need > 0:
-        workspace = _new(stream, (need,), torch.uint8, device)
-    if workspace is not None and (not workspace.is_cuda or workspace.device != device):
-        raise KataError(KATA_ERR_INVALID_ARG, f"workspace must be on {device}")
-    if workspace is not None and not workspace.is_contiguous():
+    if workspace is None:
+        return (None, 0) if need == 0 else (_new(stream, like, (need,), torch.uint8), need)
+    if workspace.device != like.device:
+        raise KataError(KATA_ERR_INVALID_ARG, f"workspace must be on {like.device}")
+    if not workspace.is_contiguous():
         raise KataError(KATA_ERR_INVALID_ARG, "workspace must be contiguous")
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _cross_inputs(q, k, v, key_lengths):
     """Checks shared by both directions; (B, H, Hkv, Tq, Tk, d)."""
     import torch
 
+    if not q.is_cuda:
+        raise KataError(KATA_ERR_INVALID_ARG, "q must be a CUDA tensor")
     for t, name in ((q, "q"), (k, "k")):
         if t.dim() != 4:
             raise KataError(KATA_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, want [B, H, T, d]")
     B, H, Tq, d = q.shape
-    Hkv, Tk = k.shape[1], k.shape[2]
-    dev = q.device
-    _check(q, "q", (B, H, Tq, d), device=dev)
-    _check(k, "k", (B, Hkv, Tk, d), q.dtype, device=dev)
-    _check(v, "v", (B, Hkv, Tk, d), q.dtype, device=dev)
-    _check(key_lengths, "key_lengths", (B,), torch.int32, device=dev)
+    _, Hkv, Tk, _ = k.shape
+    dev, dt = q.device, q.dtype
+    _is(q, "q", (B, H, Tq, d), dt, dev)
+    _is(k, "k", (B, Hkv, Tk, d), dt, dev)
+    _is(v, "v", (B, Hkv, Tk, d), dt, dev)
+    if key_lengths is not None:
+        _is(key_lengths, "key_lengths", (B,), torch.int32, dev)
     return B, H, Hkv, Tq, Tk, d
 
 
@@ -836,23 +873,21 @@ def kata_cross_forward(q, k, v, key_lengths=None, out=None, y_out=None, den_out=
     weights, which kata_cross_backward reads."""
     import torch
 
-    lib = load_library()
-    B, H, Hkv, Tq, Tk, d = _cross_inputs(q, k, v, key_lengths)
+    B, H, Hkv, Tq, Tk, d = sizes = _cross_inputs(q, k, v, key_lengths)
     dev = q.device
     code = _dtype_code(q)
     if out is None:
-        out = _new(stream, (B, H, Tq, d), q.dtype, dev)
-    _check(out, "out", (B, H, Tq, d), q.dtype, device=dev)
-    _check(y_out, "y_out", (B, H, Tq, d), torch.float32, device=dev)
-    _check(den_out, "den_out", (B, H, Tq), torch.float32, device=dev)
-    need = lib.kata_cross_forward_workspace_bytes(B, H, Hkv, Tq, Tk, d, code)
-    workspace, nbytes = _sized_workspace(workspace, need, dev, stream)
-    with _on_device(dev):
-        st = lib.kata_cross_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(key_lengths), _ptr(out), B, H,
-                                    Hkv, Tq, Tk, d, code, _ptr(y_out), _ptr(den_out),
-                                    _ptr(workspace), nbytes, _stream_handle(stream, dev))
-    if st != KATA_OK:
-        raise KataError(st, "kata_cross_forward")
+        out = _new(stream, q, (B, H, Tq, d))
+    else:
+        _is(out, "out", (B, H, Tq, d), q.dtype, dev)
+    if y_out is not None:
+        _is(y_out, "y_out", (B, H, Tq, d), torch.float32, dev)
+    if den_out is not None:
+        _is(den_out, "den_out", (B, H, Tq), torch.float32, dev)
+    need = load_library().kata_cross_forward_workspace_bytes(*sizes, code)
+    workspace, nbytes = _sized_workspace(workspace, need, q, stream)
+    _run("kata_cross_forward", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(key_lengths),
+         out.data_ptr(), *sizes, code, _address(y_out), _address(den_out), _address(workspace), nbytes)
     return out
 
 
@@ -866,31 +901,25 @@ def kata_cross_backward(dout, q, k, v, y, den, key_lengths=None, dq=None, dk=Non
     and what it wrote to y_out and den_out for the same q, k, v, key_lengths."""
     import torch
 
-    lib = load_library()
-    B, H, Hkv, Tq, Tk, d = _cross_inputs(q, k, v, key_lengths)
+    B, H, Hkv, Tq, Tk, d = sizes = _cross_inputs(q, k, v, key_lengths)
     dev = q.device
     code = _dtype_code(q)
-    _check(dout, "dout", (B, H, Tq, d), q.dtype, device=dev)
-    _check(y, "y", (B, H, Tq, d), torch.float32, device=dev)
-    _check(den, "den", (B, H, Tq), torch.float32, device=dev)
-    if dq is None:
-        dq = _new(stream, (B, H, Tq, d), q.dtype, dev)
-    if dk is None:
-        dk = _new(stream, (B, Hkv, Tk, d), q.dtype, dev)
-    if dv is None:
-        dv = _new(stream, (B, Hkv, Tk, d), q.dtype, dev)
-    _check(dq, "dq", (B, H, Tq, d), q.dtype, device=dev)
-    _check(dk, "dk", (B, Hkv, Tk, d), q.dtype, device=dev)
-    _check(dv, "dv", (B, Hkv, Tk, d), q.dtype, device=dev)
-    need = lib.kata_cross_backward_workspace_bytes(B, H, Hkv, Tq, Tk, d, code)
-    workspace, nbytes = _sized_workspace(workspace, need, dev, stream)
-    with _on_device(dev):
-        st = lib.kata_cross_backward(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(y), _ptr(den),
-                                     _ptr(key_lengths), _ptr(dq), _ptr(dk), _ptr(dv), B, H, Hkv,
-                                     Tq, Tk, d, code, _ptr(workspace), nbytes,
-                                     _stream_handle(stream, dev))
-    if st != KATA_OK:
-        raise KataError(st, "kata_cross_backward")
+    _is(dout, "dout", (B, H, Tq, d), q.dtype, dev)
+    _is(y, "y", (B, H, Tq, d), torch.float32, dev)
+    _is(den, "den", (B, H, Tq), torch.float32, dev)
+    grads = []
+    for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
+        if t is None:
+            t = _new(stream, q, like.shape)
+        else:
+            _is(t, name, like.shape, q.dtype, dev)
+        grads.append(t)
+    dq, dk, dv = grads
+    need = load_library().kata_cross_backward_workspace_bytes(*sizes, code)
+    workspace, nbytes = _sized_workspace(workspace, need, q, stream)
+    _run("kata_cross_backward", dev, stream, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+         y.data_ptr(), den.data_ptr(), _address(key_lengths), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+         *sizes, code, _address(workspace), nbytes)
     return dq, dk, dv
 
 

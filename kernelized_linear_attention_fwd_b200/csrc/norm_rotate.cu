@@ -170,19 +170,19 @@ struct NormArgs {
 // U row groups in flight per warp: at U = 4 a lane has 4 (forward) loads of 16
 // bytes outstanding, about 128 KB per SM at 64 warps.
 template <typename T, int D, bool INTER, bool BWD>
-__global__ void __launch_bounds__(32 * kNormWarps)
+__global__ void __launch_bounds__(32 * kNormWarps, BWD ? 3 : 4)
 norm_rotate_kernel(const NormArgs<T> a) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes, U = BWD ? 2 : 4;
     __shared__ float2 cs_buf[kNormWarps][32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, sub = lane / kLanes;
     Lane<D, INTER> L(lane, a.n_rot);
     const double turn_freq = lane < a.n_rot ? (double)a.inv_freq[lane] * 0.15915494309189533577 : 0.0;
-    float w[2][8];
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            w[m][e] = a.H[m] > 0 && a.w[m] ? a.w[m][(e < 4 ? L.o0 : L.o1) + (e & 3)] : 1.f;
+    __shared__ float w_buf[2][D];
+    for (int x = threadIdx.x; x < 2 * D; x += 32 * kNormWarps) {
+        const float *src = x < D ? a.w[0] : a.w[1];
+        (&w_buf[0][0])[x] = src ? src[x % D] : 1.f;
+    }
+    __syncthreads();
     float dw[2][8] = {};
 
     const long long n_warps = (long long)gridDim.x * kNormWarps;
@@ -195,6 +195,9 @@ norm_rotate_kernel(const NormArgs<T> a) {
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const int H = a.H[m];
+            float w[8];
+            *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(&w_buf[m][L.o0]);
+            *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(&w_buf[m][L.o1]);
             const T *xt = a.x[m] + b * a.sb[m] + t * a.st[m];
             const long long yt = (b * H * a.T_ + t) * D;  // head h adds h T D
             for (int h0 = blockIdx.y * (U * kRows); h0 < H; h0 += gridDim.y * (U * kRows)) {
@@ -222,12 +225,12 @@ norm_rotate_kernel(const NormArgs<T> a) {
                     const float r = rsqrtf(fmaf(row_sum<D>(ss), 1.f / D, a.eps));
                     if (!BWD) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] *= r * w[m][e];
+                        for (int e = 0; e < 8; ++e) x[e] *= w[e];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float za = x[pa<INTER>(j)], zb = x[pb<INTER>(j)];
-                            o[pa<INTER>(j)] = fmaf(za, L.c[j], -zb * L.s[j]);
-                            o[pb<INTER>(j)] = fmaf(za, L.s[j], zb * L.c[j]);
+                            o[pa<INTER>(j)] = r * fmaf(za, L.c[j], -zb * L.s[j]);
+                            o[pb<INTER>(j)] = r * fmaf(za, L.s[j], zb * L.c[j]);
                         }
                         rx[u].set(o);
                         if (h < H) rx[u].store(a.y[m] + yt + (long long)h * a.T_ * D, L.o0, L.o1);
@@ -245,7 +248,7 @@ norm_rotate_kernel(const NormArgs<T> a) {
                         for (int e = 0; e < 8; ++e) {
                             x[e] *= r;  // u
                             dw[m][e] = fmaf(g[e], x[e], dw[m][e]);
-                            g[e] *= w[m][e];
+                            g[e] *= w[e];
                             dot = fmaf(g[e], x[e], dot);
                         }
                         const float mean = row_sum<D>(dot) * (1.f / D);
@@ -281,24 +284,28 @@ norm_rotate_kernel(const NormArgs<T> a) {
     }
 }
 
-// dw = sum of the blocks' partial sums, in a fixed order: one CTA, thread (g, c)
-// adds the blocks g, g + G, ... of column c, then the G groups are added in turn.
+// dw = sum of the blocks' partial sums, in a fixed order: a CTA per 16 columns,
+// thread (g, c) adds the blocks g, g + 64, ... of column c, then one warp per column
+// adds the 64 groups.
 template <int D>
 __global__ void __launch_bounds__(1024)
 norm_dw_kernel(const float *partial, int n, float *dwq, float *dwk) {
-    constexpr int C = 2 * D, G = 1024 / C;
-    __shared__ float red[G][C];
-    const int c = threadIdx.x % C, g = threadIdx.x / C;
+    constexpr int C = 16, G = 1024 / C;  // columns and groups of a CTA
+    __shared__ float red[G][C + 1];
+    const int c = threadIdx.x % C, g = threadIdx.x / C, col = blockIdx.x * C + c;
     float v = 0.f;
-#pragma unroll 8
-    for (int i = g; i < n; i += G) v += partial[(long long)i * C + c];
+#pragma unroll 10
+    for (int i = g; i < n; i += G) v += partial[(long long)i * (2 * D) + col];
     red[g][c] = v;
     __syncthreads();
-    if (g == 0) {
-        v = 0.f;
-        for (int x = 0; x < G; ++x) v += red[x][c];
-        float *dst = c < D ? dwq : dwk;
-        if (dst) dst[c % D] = v;
+    if (threadIdx.x < 32 * C) {  // warp x: the groups of column x, always in this order
+        const int x = threadIdx.x / 32, l = threadIdx.x % 32;
+        v = red[l][x] + red[l + 32][x];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        const int k = blockIdx.x * C + x;
+        float *dst = k < D ? dwq : dwk;
+        if (l == 0 && dst) dst[k % D] = v;
     }
 }
 
@@ -337,7 +344,7 @@ cudaError_t launch_one(const NormRotate &p, cudaStream_t st) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !BWD || (!p.dw[0] && !p.dw[1])) return e;
     ProfScope prof("norm_dw", st);
-    norm_dw_kernel<D><<<1, 1024, 0, st>>>(a.partial, (int)(grid.x * grid.y), p.dw[0], p.dw[1]);
+    norm_dw_kernel<D><<<2 * D / 16, 1024, 0, st>>>(a.partial, (int)(grid.x * grid.y), p.dw[0], p.dw[1]);
     return cudaGetLastError();
 }
 
