@@ -3,12 +3,13 @@
 // partial sums when a long axis was split over several CTAs.
 #include <cuda_bf16.h>
 
+#include "cross_sched.cuh"
 #include "kata_internal.cuh"
 
 namespace kata {
 namespace {
 
-// Row statistics of the backward pass: delta = dy.y (y the forward's unrounded
+// Row statistics of the backward pass: delta = -dy.y (y the forward's unrounded
 // output) and 1 / den (0 for a row without weight), zeros in the padding up to
 // R_pad.  8 lanes per row.
 template <typename T>
@@ -36,7 +37,7 @@ cross_stats_kernel(const T *dout, const float *y, const float *den, float *delta
         const unsigned mask = 0xffu << (threadIdx.x % 32 / 8 * 8);
         for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(mask, s, o);
         if (sub == 0) {
-            delta[x] = s;
+            delta[x] = -s;
             rden[x] = rd;
         }
     }
@@ -120,6 +121,128 @@ cudaError_t launch_join(const CrossPlan &p, CrossMode mode, const float *part, c
     return cudaGetLastError();
 }
 
+// Joins the items that the tensor cores' schedule cut (cross_sched.cuh).  Grid x: the
+// stretch boundaries c = 1 .. G - 1; the block of the first boundary inside an item
+// adds the item's pieces in order: the end of CTA c - 1's stretch, then the starts
+// of the later CTAs' up to the item's end.  A block of 256 threads takes 16 / G16
+// rows (grid y), thread = 4 columns of a row and every G16-th piece.
+template <int MODE, int G16>
+__global__ void __launch_bounds__(256)
+cross_tc_join_kernel(const XSched s, const float *part, const float *part_l, const float *rden, __nv_bfloat16 *o0,
+                     __nv_bfloat16 *o1, float *y, float *den, int grid, int R_pad, int d) {
+    constexpr int TPI = cross_tc_tiles(MODE), kRows = 16 / G16;
+    __shared__ long long sh[4];  // piece range, first slot, item
+    __shared__ float4 red[16][16];
+    __shared__ float red_l[16];
+    const int c = blockIdx.x + 1;
+    if (threadIdx.x < 32) {
+        const XLine<MODE> line(s, threadIdx.x);
+        const long long n = line.share(s, grid), u = n * c;
+        long long seq0;
+        const XPos at = line.place(s, u, seq0);
+        if (threadIdx.x == 0) {
+            sh[0] = 0;
+            if (u < line.total && at.blk > 0) {
+                int live, tiles, blocks;
+                x_extent<MODE>(s, at.b, live, tiles, blocks);
+                const int nt = min(TPI, tiles - TPI * at.p);
+                const long long u0 = seq0 + (long long)at.h * tiles * blocks + (long long)at.p * TPI * blocks;
+                const long long u1 = u0 + (long long)nt * blocks;
+                // boundaries below u0 + nt are moved down to the item's start
+                if ((u0 + nt + n - 1) / n == c) {
+                    sh[0] = (u1 - 1) / n - c + 2;                          // pieces
+                    sh[1] = 2 * (c - 1) + ((long long)(c - 1) * n >= u0 ? 0 : 1);  // the first one's slot
+                    sh[2] = (long long)at.b * s.Hkv + at.h;
+                    sh[3] = (long long)at.p * TPI * 128;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const int pieces = (int)sh[0];
+    if (pieces == 0) return;
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, g = ty % G16, col = 4 * tx;
+    const int row = blockIdx.y * kRows + ty / G16;  // of the slot
+    // dkv: rows 0 .. 127 of a slot are dv's, the others dk's
+    const int r = (int)sh[3] + (MODE == kCrossDkv ? row % 128 : row);
+    const bool on = r < s.rows && row < TPI * 128 * (MODE == kCrossDkv ? 2 : 1) && col < d;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    if (on) {
+#pragma unroll 4
+        for (int x = g; x < pieces; x += G16) {
+            const long long slot = x == 0 ? sh[1] : 2LL * (c - 1 + x);
+            const long long pr = slot * s.slot_rows + row;
+            const float4 w = *reinterpret_cast<const float4 *>(part + pr * d + col);
+            v.x += w.x;
+            v.y += w.y;
+            v.z += w.z;
+            v.w += w.w;
+            if (MODE == kCrossFwd) l += part_l[pr];
+        }
+    }
+    if (G16 > 1) {
+        red[ty][tx] = v;
+        if (MODE == kCrossFwd && tx == 0) red_l[ty] = l;
+        __syncthreads();
+        if (g > 0) return;
+        for (int x = 1; x < G16; ++x) {
+            const float4 w = red[ty + x][tx];
+            v.x += w.x;
+            v.y += w.y;
+            v.z += w.z;
+            v.w += w.w;
+        }
+        if (MODE == kCrossFwd) {
+            l = red_l[ty];
+            for (int x = 1; x < G16; ++x) l += red_l[ty + x];
+        }
+    }
+    if (!on) return;
+    float f = 1.f;
+    if (MODE == kCrossFwd) f = cross_recip(l);
+    if (MODE == kCrossDq) f = 2.f * rden[sh[2] * R_pad + r];
+    if (MODE == kCrossDkv && row >= 128) f = 2.f;
+    v.x *= f;
+    v.y *= f;
+    v.z *= f;
+    v.w *= f;
+    const long long gr = sh[2] * s.rows + r, o = gr * d + col;
+    __nv_bfloat16 *dst = MODE == kCrossDkv && row >= 128 ? o1 : o0;
+    __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2 *>(dst + o) =
+        make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
+    if (MODE == kCrossFwd) {
+        if (y) *reinterpret_cast<float4 *>(y + o) = v;
+        if (den && col == 0) den[gr] = l;
+    }
+}
+
+template <int MODE>
+cudaError_t launch_tc_join(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    XSched s = p.sched[MODE];
+    s.key_lengths = io.key_lengths;
+    if (s.whole || s.grid == 1) return cudaSuccess;
+    char *ws = static_cast<char *>(io.ws);
+    const float *part = reinterpret_cast<const float *>(ws + p.ws_part[MODE]);
+    const float *part_l = reinterpret_cast<const float *>(ws + p.ws_part_l);
+    const float *rden = reinterpret_cast<const float *>(ws + p.ws_rden);
+    __nv_bfloat16 *o0 =
+        static_cast<__nv_bfloat16 *>(MODE == kCrossFwd ? io.out : MODE == kCrossDq ? io.dq : io.dv);
+    __nv_bfloat16 *o1 = static_cast<__nv_bfloat16 *>(io.dk);
+    // few rows: an item is cut into many pieces, which 16 threads share per 4 columns
+    const bool few = s.slot_rows <= 64;
+    const dim3 grid(s.grid - 1, few ? s.slot_rows : (s.slot_rows + 15) / 16);
+    ProfScope prof("cross_join", st);
+    if (few)
+        cross_tc_join_kernel<MODE, 16><<<grid, 256, 0, st>>>(s, part, part_l, rden, o0, o1, io.y, io.den, s.grid,
+                                                              p.R_pad, p.d);
+    else
+        cross_tc_join_kernel<MODE, 1><<<grid, 256, 0, st>>>(s, part, part_l, rden, o0, o1, io.y, io.den, s.grid,
+                                                             p.R_pad, p.d);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_main(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     return p.dtype == KATA_BF16 ? launch_cross_tc(mode, p, io, st) : launch_cross_simt(mode, p, io, st);
 }
@@ -127,6 +250,7 @@ cudaError_t launch_main(CrossMode mode, const CrossPlan &p, const CrossIo &io, c
 template <typename T>
 cudaError_t forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     cudaError_t e = launch_main(kCrossFwd, p, io, st);
+    if (e == cudaSuccess && p.dtype == KATA_BF16) return launch_tc_join<kCrossFwd>(p, io, st);
     if (e != cudaSuccess || p.splits[kCrossFwd] == 1) return e;
     const char *ws = static_cast<const char *>(io.ws);
     return launch_join<T, kJoinDen>(p, kCrossFwd, reinterpret_cast<const float *>(ws + p.ws_part[kCrossFwd]),
@@ -147,6 +271,11 @@ cudaError_t backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if ((e = launch_main(kCrossDq, p, io, st)) != cudaSuccess) return e;
+    if (p.dtype == KATA_BF16) {
+        if ((e = launch_tc_join<kCrossDq>(p, io, st)) != cudaSuccess) return e;
+        if ((e = launch_main(kCrossDkv, p, io, st)) != cudaSuccess) return e;
+        return launch_tc_join<kCrossDkv>(p, io, st);
+    }
     if (p.splits[kCrossDq] > 1) {
         e = launch_join<T, kJoinRow>(p, kCrossDq, reinterpret_cast<const float *>(ws + p.ws_part[kCrossDq]), nullptr,
                                      rden, io.dq, nullptr, nullptr, p.BH * p.R, p.BH * p.R, st);
@@ -165,11 +294,6 @@ cudaError_t backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
 }
 
 }  // namespace
-
-CrossTile cross_tile(CrossMode mode, const CrossPlan &p) {
-    if (p.dtype == KATA_BF16) return {256, mode == kCrossFwd ? 128 : 64};
-    return {mode == kCrossFwd && p.R <= 16 ? 16 : 64, 64};
-}
 
 cudaError_t launch_cross_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     return p.dtype == KATA_BF16 ? forward<__nv_bfloat16>(p, io, st) : forward<float>(p, io, st);

@@ -1,0 +1,215 @@
+// How the tensor-core cross attention shares its work out (cross_tc.cu), and which
+// pieces of an item the join adds up (cross.cu).
+//
+// The work of one mode is a line of units (128-row tile, column block): sequence b
+// has Hkv T_b N_b of them, T_b row tiles and N_b column blocks; in the forward and
+// dq passes N_b follows the sequence's visible keys, in dkv T_b does.  Items are
+// one or two tiles of one head; CTA c of G takes the units [c S, (c + 1) S),
+// S = max(ceil(total / G), min_share), cut at block boundaries (an item of two
+// tiles steps two units at a time; a cut inside one is moved down).  So every CTA
+// has the same work to within a block whatever the lengths are, and few long items
+// are split over all CTAs.  Plans whose items fill the grid many times over do not
+// cut (whole): there the cuts are moved down to item boundaries.
+#pragma once
+
+#include "kata_internal.cuh"
+
+namespace kata {
+
+__host__ __device__ constexpr int cross_tc_cols(int mode) { return mode == kCrossFwd ? 128 : 64; }
+__host__ __device__ constexpr int cross_tc_tiles(int mode) { return mode == kCrossDkv ? 1 : 2; }
+
+// A place in the line: block `blk` of item `p` of head `h` of sequence `b`.
+struct XPos {
+    int b, h, p, blk;
+};
+struct XRange {
+    XPos from, to;
+};
+// A stretch of blocks of one item.
+struct XItem {
+    int bh, r0, n_tiles, b0, n_blk;
+    int cols;  // columns in use (dkv: all of them)
+    int live;  // visible keys of the sequence
+    int part;  // slot of a cut item's piece, or -1
+};
+
+// T_b and N_b.
+template <int MODE>
+__device__ __forceinline__ void x_extent(const XSched &s, int b, int &live, int &tiles, int &blocks) {
+    live = cross_length(s.key_lengths, b, s.Tk);
+    const int rows = MODE == kCrossDkv ? live : s.rows, cols = MODE == kCrossDkv ? s.cols : live;
+    tiles = (rows + 127) / 128;
+    blocks = (cols + cross_tc_cols(MODE) - 1) / cross_tc_cols(MODE);
+}
+
+// Place of unit `off` of sequence b.
+template <int MODE>
+__device__ __forceinline__ XPos x_place(const XSched &s, int b, long long off, int tiles, int blocks) {
+    constexpr int TPI = cross_tc_tiles(MODE);
+    const long long per_head = (long long)tiles * blocks;
+    XPos r;
+    r.b = b;
+    r.h = (int)(off / per_head);
+    const long long rem = off - r.h * per_head;
+    r.p = (int)(rem / ((long long)TPI * blocks));
+    const int in_item = (int)(rem - r.p * ((long long)TPI * blocks));
+    const int nt = min(TPI, tiles - TPI * r.p);
+    r.blk = s.whole ? 0 : in_item / nt;
+    return r;
+}
+
+// The whole line as one warp sees it: every lane holds the units of a run of
+// sequences.  Call with all 32 lanes.
+template <int MODE>
+struct XLine {
+    long long before, units, total;  // units before this lane's run, in it, in all
+    int first, last;                 // the run
+
+    __device__ __forceinline__ XLine(const XSched &s, int lane) {
+        if (!s.key_lengths) {  // all sequences alike: lane 0 holds them
+            int live, tiles, blocks;
+            x_extent<MODE>(s, 0, live, tiles, blocks);
+            total = (long long)s.B * s.Hkv * tiles * blocks;
+            units = lane == 0 ? total : 0;
+            before = lane == 0 ? 0 : total;
+            first = lane == 0 ? 0 : s.B;
+            last = s.B;
+            return;
+        }
+        const int run = (s.B + 31) / 32;
+        first = min(s.B, lane * run);
+        last = min(s.B, first + run);
+        units = 0;
+        for (int b = first; b < last; ++b) {
+            int live, tiles, blocks;
+            x_extent<MODE>(s, b, live, tiles, blocks);
+            units += (long long)s.Hkv * tiles * blocks;
+        }
+        long long sum = units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        before = sum - units;
+        total = __shfl_sync(0xffffffffu, sum, 31);
+    }
+
+    __device__ __forceinline__ long long share(const XSched &s, int grid) const {
+        const long long n = (total + grid - 1) / grid;
+        return n < s.min_share ? s.min_share : n;
+    }
+
+    // Place of unit u; also the units before its sequence.
+    __device__ __forceinline__ XPos place(const XSched &s, long long u, long long &seq0) const {
+        XPos r = {s.B, 0, 0, 0};
+        seq0 = total;
+        const bool mine = u < total && u >= before && u < before + units;
+        if (mine) {
+            long long at = before;
+            if (!s.key_lengths) {
+                int live, tiles, blocks;
+                x_extent<MODE>(s, 0, live, tiles, blocks);
+                const long long per = (long long)s.Hkv * tiles * blocks;
+                const int b = (int)(u / per);
+                seq0 = b * per;
+                r = x_place<MODE>(s, b, u - seq0, tiles, blocks);
+            } else {
+                for (int b = first; b < last; ++b) {
+                    int live, tiles, blocks;
+                    x_extent<MODE>(s, b, live, tiles, blocks);
+                    const long long per = (long long)s.Hkv * tiles * blocks;
+                    if (u < at + per) {
+                        seq0 = at;
+                        r = x_place<MODE>(s, b, u - at, tiles, blocks);
+                        break;
+                    }
+                    at += per;
+                }
+            }
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, mine);
+        const int src = who ? __ffs(who) - 1 : 0;
+        r.b = __shfl_sync(0xffffffffu, r.b, src);
+        r.h = __shfl_sync(0xffffffffu, r.h, src);
+        r.p = __shfl_sync(0xffffffffu, r.p, src);
+        r.blk = __shfl_sync(0xffffffffu, r.blk, src);
+        seq0 = __shfl_sync(0xffffffffu, seq0, src);
+        return r;
+    }
+};
+
+// CTA c's stretch.  All 32 lanes.
+template <int MODE>
+__device__ __forceinline__ XRange x_range(const XSched &s, int c, int grid, int lane) {
+    const XLine<MODE> line(s, lane);
+    const long long n = line.share(s, grid);
+    long long unused;
+    XRange r;
+    r.from = line.place(s, n * c, unused);
+    r.to = line.place(s, n * (c + 1), unused);
+    return r;
+}
+
+template <int MODE>
+struct XIter {
+    const XSched &s;
+    XPos at, to;
+    int pieces = 0;
+
+    __device__ __forceinline__ XIter(const XSched &s_, const XRange &r) : s(s_), at(r.from), to(r.to) {}
+
+    __device__ __forceinline__ bool next(XItem &it) {
+        constexpr int TPI = cross_tc_tiles(MODE);
+        while (at.b < s.B) {
+            if (at.b == to.b && at.h == to.h && at.p == to.p && at.blk == to.blk) return false;
+            int live, tiles, blocks;
+            x_extent<MODE>(s, at.b, live, tiles, blocks);
+            if (tiles == 0 || blocks == 0) {  // no unit (never where a stretch starts or ends)
+                ++at.b;
+                continue;
+            }
+            const bool cut = at.b == to.b && at.h == to.h && at.p == to.p;
+            const int end = cut ? to.blk : blocks;
+            it.bh = at.b * s.Hkv + at.h;
+            it.r0 = at.p * TPI * 128;
+            it.n_tiles = min(TPI, tiles - TPI * at.p);
+            it.b0 = at.blk;
+            it.n_blk = end - at.blk;
+            it.cols = MODE == kCrossDkv ? s.cols : live;
+            it.live = live;
+            it.part = at.blk == 0 && end == blocks ? -1 : 2 * (int)blockIdx.x + (pieces ? 1 : 0);
+            ++pieces;
+            if (cut) {
+                at.blk = end;
+            } else {
+                at.blk = 0;
+                if (++at.p * TPI >= tiles) {
+                    at.p = 0;
+                    if (++at.h == s.Hkv) {
+                        at.h = 0;
+                        ++at.b;
+                    }
+                }
+            }
+            return true;
+        }
+        return false;
+    }
+};
+
+// The half (warps 0-3 or 4-7) that takes step n: tile t of the CTA's j-th item.
+template <int MODE>
+__device__ __forceinline__ int x_half(const XItem &it, int t, int j, int n) {
+    if (MODE == kCrossDkv) return n & 1;
+    return it.n_tiles == 2 ? t : j & 1;
+}
+
+// First row of a slot in the partial sums.
+template <int MODE>
+__device__ __forceinline__ long long x_part_row(const XSched &s, int part) {
+    return (long long)part * s.slot_rows;
+}
+
+}  // namespace kata

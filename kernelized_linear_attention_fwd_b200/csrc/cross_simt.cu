@@ -117,7 +117,7 @@ cross_simt_kernel(const SArgs a) {
     const int b0 = split * piece, b1 = min(blocks, b0 + piece);
     const long long row0 = (long long)bh * a.rows + r0, col0 = (long long)bh * a.cols;
 
-    float acc0[RT][N] = {}, acc1[RT][N] = {}, l[RT] = {}, delta[RT] = {};
+    float acc0[RT][N] = {}, acc1[RT][N] = {}, l[RT] = {}, delta[RT] = {};  // delta: -D
     if (b0 < b1) {
         load_tile<D>(R0, a.r0 + row0 * D, TR, rows - r0);
         if (MODE != kCrossFwd) load_tile<D>(R1, a.r1 + row0 * D, TR, rows - r0);
@@ -153,11 +153,11 @@ cross_simt_kernel(const SArgs a) {
                     lb += w;
                     P[o] = w;
                 } else if (MODE == kCrossDq) {
-                    P[o] = s[i][j] * (g[i][j] - delta[i]);
+                    P[o] = s[i][j] * (g[i][j] + delta[i]);
                 } else {
                     const float t = s[i][j] * sr[tx + 16 * j];
                     P[o] = s[i][j] * t;
-                    E[o] = 2.f * t * (g[i][j] - sd[tx + 16 * j]);
+                    E[o] = 2.f * t * (g[i][j] + sd[tx + 16 * j]);
                 }
             }
             l[i] += lb;
@@ -241,11 +241,13 @@ template <int D>
 cudaError_t launch_d(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     if (mode == kCrossDq) return launch_one<D, kCrossDq, 4>(p, io, st);
     if (mode == kCrossDkv) return launch_one<D, kCrossDkv, 4>(p, io, st);
-    return cross_tile(mode, p).rows == 16 ? launch_one<D, kCrossFwd, 1>(p, io, st)
+    return cross_simt_rows(mode, p) == 16 ? launch_one<D, kCrossFwd, 1>(p, io, st)
                                           : launch_one<D, kCrossFwd, 4>(p, io, st);
 }
 
 }  // namespace
+
+int cross_simt_rows(CrossMode mode, const CrossPlan &p) { return mode == kCrossFwd && p.R <= 16 ? 16 : 64; }
 
 cudaError_t launch_cross_simt(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     switch (p.d) {

@@ -215,17 +215,27 @@ cudaError_t launch_norm_rotate(const NormRotate &p, cudaStream_t st);
 // heads that share a key head are consecutive in memory, so they are the rows of
 // one problem: BH = B Hkv problems of R = (H / Hkv) Tq rows and Tk keys.
 enum CrossMode : int { kCrossFwd = 0, kCrossDq = 1, kCrossDkv = 2 };
+// Work of one mode on the tensor cores (cross_sched.cuh).
+struct XSched {
+    int B, Hkv, rows, cols, Tk;
+    const int *key_lengths;
+    int grid;
+    int min_share;  // fewest units a CTA takes
+    int whole;      // cut at item boundaries only
+    int slot_rows;  // rows of a cut piece's partial sums
+};
 struct CrossPlan {
     int B, H, Hkv, Tq, Tk, d;
     kata_dtype dtype;
     long long BH;
     int R;             // rows per problem
     int R_pad;         // R rounded up to 64: row stride of the statistics
-    int splits[3];     // per CrossMode: pieces of the summed axis (1: no join)
+    int splits[3];     // fp32, per CrossMode: pieces of the summed axis (1: no join)
+    XSched sched[3];   // bf16, per CrossMode
     // workspace (bytes)
     size_t ws_part[3];  // partial sums of each mode
     size_t ws_part_l;   // forward: partial denominators
-    size_t ws_delta;    // backward: [BH][R_pad] dy.y, then [BH][R_pad] 1 / den
+    size_t ws_delta;    // backward: [BH][R_pad] -(dy.y), then [BH][R_pad] 1 / den
     size_t ws_rden;
     size_t ws_fwd_bytes, ws_bwd_bytes;
 };
@@ -242,11 +252,8 @@ cudaError_t launch_cross_backward(const CrossPlan &p, const CrossIo &io, cudaStr
 // One mode's main kernel: bf16 on the tensor cores, fp32 on the CUDA cores.
 cudaError_t launch_cross_tc(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 cudaError_t launch_cross_simt(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
-// Row and column extents of a mode's work: rows per item and columns per step.
-struct CrossTile {
-    int rows, cols;
-};
-CrossTile cross_tile(CrossMode mode, const CrossPlan &p);
+// Rows per CTA of the fp32 kernels.
+int cross_simt_rows(CrossMode mode, const CrossPlan &p);
 
 // Keys that sequence b may attend to: its length, within [0, Tk].
 __device__ __forceinline__ int cross_length(const int *key_lengths, int b, int Tk) {

@@ -2,6 +2,7 @@
 // plans and dispatch.  Declarations and the contract: include/kata.h.
 #include <math.h>
 
+#include "cross_sched.cuh"
 #include "kata_internal.cuh"
 
 namespace kata {
@@ -154,6 +155,33 @@ int cross_splits(long long items, long long steps, int min_steps) {
     return s < 1 ? 1 : (int)s;
 }
 
+// The tensor cores' schedule of one mode.  Items are cut unless that gains little:
+// when whole items, dealt evenly, leave the busiest SM at most 3% more than the
+// average (many items, or a multiple of the grid), the join is not worth its launch.
+// A CTA takes at least 4 units (forward: 512 keys of a tile) of a cut item: below
+// that its start and the join cost more than the steps it saves.
+bool cross_sched(const CrossPlan &p, CrossMode m, int rows, int cols, XSched &s) {
+    const long long tiles = (rows + 127) / 128, tpi = cross_tc_tiles(m);
+    const long long blocks = (cols + cross_tc_cols(m) - 1) / cross_tc_cols(m);
+    const long long items = p.BH * ((tiles + tpi - 1) / tpi);
+    if (items >= (1LL << 31) || p.BH > (1LL << 62) / tiles / blocks) return false;
+    const long long units = p.BH * tiles * blocks;
+    s.B = p.B;
+    s.Hkv = p.Hkv;
+    s.rows = rows;
+    s.cols = cols;
+    s.Tk = p.Tk;
+    s.key_lengths = nullptr;
+    s.min_share = 4;
+    const long long rounds = (items + kPlanSms - 1) / kPlanSms;
+    s.whole = rounds * kPlanSms * 100 <= items * 103 || (items < kPlanSms && blocks * tpi <= s.min_share);
+    const long long most = s.whole ? items : (units + s.min_share - 1) / s.min_share;
+    s.grid = (int)(most < kPlanSms ? most : kPlanSms);
+    if (s.whole) s.min_share = 1;
+    s.slot_rows = m == kCrossDkv ? 256 : rows < 256 ? rows : 256;  // dkv: dv's 128 rows and dk's
+    return true;
+}
+
 kata_status cross_plan(int B, int H, int Hkv, int Tq, int Tk, int d, kata_dtype dtype, CrossPlan &p) {
     if (B < 1 || H < 1 || Hkv < 1 || Tq < 1 || Tk < 1 || d < 1 || H % Hkv != 0) return KATA_ERR_INVALID_ARG;
     if (dtype != KATA_F32 && dtype != KATA_BF16) return KATA_ERR_UNSUPPORTED;
@@ -171,23 +199,29 @@ kata_status cross_plan(int B, int H, int Hkv, int Tq, int Tk, int d, kata_dtype 
     if (p.BH > (1LL << 40) / rows || p.BH > (1LL << 40) / Tk) return KATA_ERR_UNSUPPORTED;
     p.R = (int)rows;
     p.R_pad = (p.R + 63) / 64 * 64;
-    size_t off = 0;
+    const size_t stat = align_up((size_t)p.BH * p.R_pad * 4);
+    p.ws_delta = 0;
+    p.ws_rden = stat;
+    size_t off = 2 * stat;
     for (const CrossMode m : {kCrossFwd, kCrossDq, kCrossDkv}) {
-        const CrossTile t = cross_tile(m, p);
         const long long n = m == kCrossDkv ? Tk : p.R, c = m == kCrossDkv ? p.R : Tk;
-        const long long items = p.BH * ((n + t.rows - 1) / t.rows);
-        if (items >= most) return KATA_ERR_UNSUPPORTED;
-        p.splits[m] = cross_splits(items, (c + t.cols - 1) / t.cols, 2);
-        const size_t part =
-            p.splits[m] > 1 ? align_up((size_t)p.splits[m] * p.BH * n * d * (m == kCrossDkv ? 8 : 4)) : 0;
+        size_t part_rows = 0;  // rows of partial sums
+        if (dtype == KATA_BF16) {
+            if (!cross_sched(p, m, (int)n, (int)c, p.sched[m])) return KATA_ERR_UNSUPPORTED;
+            part_rows = p.sched[m].whole ? 0 : (size_t)p.sched[m].grid * 2 * p.sched[m].slot_rows;
+            p.splits[m] = 1;
+        } else {
+            const int t = cross_simt_rows(m, p);
+            const long long items = p.BH * ((n + t - 1) / t);
+            if (items >= most) return KATA_ERR_UNSUPPORTED;
+            p.splits[m] = cross_splits(items, (c + 63) / 64, 2);
+            if (p.splits[m] > 1) part_rows = (size_t)p.splits[m] * p.BH * n * (m == kCrossDkv ? 2 : 1);
+        }
+        const size_t part = align_up(part_rows * d * 4);
         if (m == kCrossFwd) {
             p.ws_part[m] = 0;
             p.ws_part_l = part;
-            p.ws_fwd_bytes = part + (part ? align_up((size_t)p.splits[m] * p.BH * n * 4) : 0);
-            const size_t stat = align_up((size_t)p.BH * p.R_pad * 4);
-            p.ws_delta = 0;
-            p.ws_rden = stat;
-            off = 2 * stat;
+            p.ws_fwd_bytes = part + align_up(part_rows * 4);
         } else {
             p.ws_part[m] = off;
             off += part;
