@@ -4,7 +4,7 @@
 // The work of one mode is a line of units (128-row tile, column block): sequence b
 // has Hkv T_b N_b of them, T_b row tiles and N_b column blocks; in the forward and
 // dq passes N_b follows the sequence's visible keys, in dkv T_b does.  Items are
-// one or two tiles of one head; CTA c of G takes the units [c S, (c + 1) S),
+// one tile of one head (backward) or two (forward); CTA c of G takes the units [c S, (c + 1) S),
 // S = max(ceil(total / G), min_share), cut at block boundaries (an item of two
 // tiles steps two units at a time; a cut inside one is moved down).  So every CTA
 // has the same work to within a block whatever the lengths are, and few long items
@@ -16,8 +16,8 @@
 
 namespace kata {
 
-__host__ __device__ constexpr int cross_tc_cols(int mode) { return mode == kCrossFwd ? 128 : 64; }
-__host__ __device__ constexpr int cross_tc_tiles(int mode) { return mode == kCrossDkv ? 1 : 2; }
+constexpr int kXCols = 128;  // columns of a block
+__host__ __device__ constexpr int cross_tc_tiles(int mode) { return mode == kCrossFwd ? 2 : 1; }
 
 // A place in the line: block `blk` of item `p` of head `h` of sequence `b`.
 struct XPos {
@@ -40,7 +40,7 @@ __device__ __forceinline__ void x_extent(const XSched &s, int b, int &live, int 
     live = cross_length(s.key_lengths, b, s.Tk);
     const int rows = MODE == kCrossDkv ? live : s.rows, cols = MODE == kCrossDkv ? s.cols : live;
     tiles = (rows + 127) / 128;
-    blocks = (cols + cross_tc_cols(MODE) - 1) / cross_tc_cols(MODE);
+    blocks = (cols + kXCols - 1) / kXCols;
 }
 
 // Place of unit `off` of sequence b.
@@ -199,15 +199,10 @@ struct XIter {
     }
 };
 
-// The half (warps 0-3 or 4-7) that takes step n: tile t of the CTA's j-th item.
-template <int MODE>
-__device__ __forceinline__ int x_half(const XItem &it, int t, int j, int n) {
-    if (MODE == kCrossDkv) return n & 1;
-    return it.n_tiles == 2 ? t : j & 1;
-}
+// The half (warps 0-3 or 4-7) of the forward that takes tile t of the CTA's j-th item.
+__device__ __forceinline__ int x_half(const XItem &it, int t, int j) { return it.n_tiles == 2 ? t : j & 1; }
 
 // First row of a slot in the partial sums.
-template <int MODE>
 __device__ __forceinline__ long long x_part_row(const XSched &s, int part) {
     return (long long)part * s.slot_rows;
 }

@@ -1,0 +1,379 @@
+// Backward passes of cross attention on the tensor cores (formulas, roundings and
+// work distribution: cross_tc.cu).
+//
+// A step is a 128-row tile against a block of 128 columns: two products form the
+// scores S and P (128 columns of tensor memory each), 8 warps turn them into bf16
+// weights, and one (dq) or two (dkv) products accumulate.  Tensor memory holds
+//
+//   0 .. 127    accumulators: dq: two of 64 columns, items in turn; dkv: dV, dK
+//   128, 256    S of even and odd steps; the weights replace it, per 32 scores the
+//               16 columns of ds (dq) or of w / l and ds (dkv)
+//   384         P, free again once the warps have read it
+//
+// so the next step's S is formed while this step's scores are turned, its P right
+// after them, and a step's accumulation overlaps the next one's scores.  128-column
+// score products run at the full rate (N = 64 ones pay for reading the 128-row
+// operand twice as often: a 64-column form of these kernels took 1.6 times as long).
+// Warp 8 loads, warp 9 issues S, warp 10 issues P, warps 11 and 12 accumulate (dq:
+// 11 only).  Warps 0-3 turn columns 0 .. 63 of a step, warps 4-7 columns 64 .. 127.
+#include "cross_tc.cuh"
+
+namespace kata {
+namespace {
+
+constexpr int kBThreads = 416;
+constexpr int kBTma = 8, kBS = 9, kBP = 10, kBAcc = 11;
+constexpr int kBSlot = 2 * 16384;    // an item's two row operands
+constexpr int kBOp = kXCols * 128;   // one column operand of a block
+constexpr int kBStage = 2 * kBOp;
+constexpr int kBStat = 1024;         // dkv: -D and 1 / l of the block's queries
+constexpr int kBStages = 4;
+constexpr int kBSmem = 2 * kBSlot + kBStages * (kBStage + kBStat) + 1024;
+constexpr uint32_t kBColS = 128, kBColP = 384;
+
+struct BBars {
+    uint64_t qfull[2], qempty[2], full[kBStages], empty[kBStages];
+    // per S region: scores formed, weights stored, products done; P formed, P read
+    uint64_t sfull[2], wfull[2], sfree[2], pfull, pfree;
+    uint64_t ofull[2], ofree[2], drain[4];
+};
+
+template <int MODE>
+__global__ void __launch_bounds__(kBThreads, 1)
+cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant__ CUtensorMap tm_r1,
+                 const __grid_constant__ CUtensorMap tm_c0, const __grid_constant__ CUtensorMap tm_c1,
+                 const XArgs a) {
+    constexpr bool kDkv = MODE == kCrossDkv;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ BBars bars;
+    __shared__ XRange range;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sm_ring = sm + 2 * kBSlot;
+    uint8_t *sm_stat = sm_ring + kBStages * kBStage;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.qfull[i], 1);
+            mbar_init(&bars.qempty[i], 2);  // both score warps
+            mbar_init(&bars.sfull[i], 1);
+            mbar_init(&bars.wfull[i], 8);
+            mbar_init(&bars.sfree[i], kDkv ? 2 : 1);
+            mbar_init(&bars.ofull[i], 1);
+            mbar_init(&bars.ofree[i], kDkv ? 4 : 8);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(&bars.drain[i], 1);
+        for (int i = 0; i < kBStages; ++i) {
+            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.empty[i], 1);
+        }
+        mbar_init(&bars.pfull, 1);
+        mbar_init(&bars.pfree, 8);
+        fence_mbarrier_init();
+    }
+    if (warp == kBS) {
+        tmem_alloc(&tmem_base, 512);
+        tmem_relinquish();
+    }
+    if (warp == kBTma) {
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_r0);
+            tma_prefetch_desc(&tm_r1);
+            tma_prefetch_desc(&tm_c0);
+            tma_prefetch_desc(&tm_c1);
+        }
+        __syncwarp();
+        const XRange r = x_range<MODE>(a.sched, blockIdx.x, gridDim.x, lane);
+        if (lane == 0) range = r;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem_base;
+    volatile int *abort = &abort_flag;
+    XIter<MODE> iter(a.sched, range);
+    XItem it;
+
+    if (warp == kBTma) {
+        // ------------------------------------------------------------ loads
+        if (lane == 0) {
+            int nq = 0, ns = 0;  // items and stages loaded
+            XRing stage;
+            bool ok = true;
+            while (ok && iter.next(it)) {
+                const int qb = nq & 1;
+                ok = mbar_wait(&bars.qempty[qb], ((nq >> 1) & 1) ^ 1, abort);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&bars.qfull[qb], kBSlot);
+                tma_load_3d(sm + qb * kBSlot, &tm_r0, &bars.qfull[qb], 0, it.r0, it.bh);
+                tma_load_3d(sm + qb * kBSlot + 16384, &tm_r1, &bars.qfull[qb], 0, it.r0, it.bh);
+                ++nq;
+                for (int b = 0; b < it.n_blk; ++b) {
+                    const int s = stage.i;
+                    ok = mbar_wait(&bars.empty[s], stage.phase ^ 1, abort);
+                    if (!ok) break;
+                    const int col = (it.b0 + b) * kXCols;
+                    uint8_t *dst = sm_ring + s * kBStage;
+                    // boxes of 64 columns; dq skips a second one without a visible key
+                    const int boxes = kDkv || it.cols - col > 64 ? 2 : 1;
+                    mbar_arrive_expect_tx(&bars.full[s], boxes * 16384 + (kDkv ? kBStat : 0));
+                    for (int x = 0; x < boxes; ++x) {
+                        tma_load_3d(dst + x * 8192, &tm_c0, &bars.full[s], 0, col + 64 * x, it.bh);
+                        tma_load_3d(dst + kBOp + x * 8192, &tm_c1, &bars.full[s], 0, col + 64 * x, it.bh);
+                    }
+                    if (kDkv) {
+                        const long long o = (long long)it.bh * a.stat_stride + col;
+                        bulk_load(sm_stat + s * kBStat, a.delta + o, 512, &bars.full[s]);
+                        bulk_load(sm_stat + s * kBStat + 512, a.rden + o, 512, &bars.full[s]);
+                    }
+                    ++ns;
+                    stage.next(kBStages);
+                }
+            }
+            // every load issued must have landed before the CTA exits
+            for (int x = nq > 2 ? nq - 2 : 0; x < nq; ++x) mbar_wait_issued(&bars.qfull[x & 1], (x >> 1) & 1);
+            for (int x = ns > kBStages ? ns - kBStages : 0; x < ns; ++x)
+                mbar_wait_issued(&bars.full[x % kBStages], (x / kBStages) & 1);
+        }
+    } else if (warp == kBS || warp == kBP) {
+        // ------------------------------------------------------------ products that form S, P
+        if (lane == 0) {
+            const int me = warp - kBS;
+            const uint32_t id = idesc_bf16(128, 128, 0, 0);
+            const uint64_t dR = desc_sw128(smem_u32(sm + 16384 * me), 16, 1024);
+            const uint64_t dC = desc_sw128(smem_u32(sm_ring + kBOp * me), 16, 1024);
+            const int n_ks = a.d / 16;  // the head's own coordinates: the columns past d are zeros
+            XRing stage, buf;           // buf: S region (two), or the one of P
+            int j = 0;
+            uint32_t release = 0;  // warp kBS, per S region (4 bits): the stage + 1 its step reads
+            bool ok = true;
+            while (ok && iter.next(it)) {
+                const int qb = j & 1;
+                const uint64_t r = desc_at(dR, qb * kBSlot);
+                ok = mbar_wait(&bars.qfull[qb], (j >> 1) & 1, abort);
+                for (int b = 0; b < it.n_blk && ok; ++b) {
+                    const uint64_t c = desc_at(dC, stage.i * kBStage);
+                    const uint32_t col = tm + (me == 0 ? kBColS + 128 * buf.i : kBColP);
+                    const uint32_t done = (release >> (4 * buf.i)) & 15u;
+                    release = (release & ~(15u << (4 * buf.i))) | ((stage.i + 1u) << (4 * buf.i));
+                    ok = mbar_wait(&bars.full[stage.i], stage.phase, abort) &&
+                         mbar_wait(me == 0 ? &bars.sfree[buf.i] : &bars.pfree, buf.phase ^ 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        if (ks < n_ks) mma_ss(col, desc_at(r, 32 * ks), desc_at(c, 32 * ks), id, ks > 0);
+                    mma_commit(me == 0 ? &bars.sfull[buf.i] : &bars.pfull);
+                    // a region found free: every product of the step that used it is done, so
+                    // its stage is (P of that step was formed before its weights)
+                    if (me == 0 && done) mbar_arrive(&bars.empty[done - 1]);
+                    buf.next(me == 0 ? 2 : 1);
+                    stage.next(kBStages);
+                }
+                if (!ok) break;
+                mma_commit(&bars.qempty[qb]);
+                ++j;
+            }
+            mma_commit(&bars.drain[me]);
+            mbar_wait_issued(&bars.drain[me], 0);
+        }
+    } else if (warp >= kBAcc) {
+        // ------------------------------------------------------------ products that accumulate
+        if (lane == 0 && (kDkv || warp == kBAcc)) {
+            const int me = warp - kBAcc;  // dkv: 0: dV from w / l and dY, 1: dK from ds and Q
+            const uint32_t id = idesc_bf16(128, 64, 0, 1);
+            const uint64_t dC = desc_sw128(smem_u32(sm_ring + (kDkv && me == 0 ? kBOp : 0)), 8192, 1024);
+            XRing stage, buf, acc;  // acc: dq, the accumulator of the item
+            uint32_t ophase = 1;    // dkv: the accumulator's first use passes at once
+            bool ok = true;
+            while (ok && iter.next(it)) {
+                const int o = kDkv ? me : acc.i;
+                ok = mbar_wait(&bars.ofree[o], kDkv ? ophase : acc.phase ^ 1, abort);
+                for (int b = 0; b < it.n_blk && ok; ++b) {
+                    const uint64_t c = desc_at(dC, stage.i * kBStage);
+                    const uint32_t w = tm + kBColS + 128 * buf.i + 16 * me;
+                    ok = mbar_wait(&bars.wfull[buf.i], buf.phase, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ts(tm + 64 * o, w + 32 * (ks / 2) + 8 * (ks % 2), desc_at(c, 2048 * ks), id,
+                               b > 0 || ks > 0);
+                    mma_commit(&bars.sfree[buf.i]);
+                    buf.next(2);
+                    stage.next(kBStages);
+                }
+                if (!ok) break;
+                mma_commit(&bars.ofull[o]);
+                ophase ^= 1;
+                acc.next(2);
+            }
+            mma_commit(&bars.drain[2 + me]);
+            mbar_wait_issued(&bars.drain[2 + me], 0);
+        }
+    } else {
+        // ------------------------------------------------------------ weights and epilogue
+        const int half = warp / 4, qd = warp % 4;
+        const int row = 32 * qd + lane;
+        const uint32_t lane_base = static_cast<uint32_t>(32 * qd) << 16;
+        const int rows = a.sched.rows;
+        const uint32_t tP = tm + kBColP + 64 * half + lane_base;
+        XRing stage, buf, acc;
+        uint32_t pphase = 0, ophase = 0;
+        bool ok = true;
+        zero_dead_rows<MODE>(a, warp, lane);
+        __syncwarp();
+        while (ok && iter.next(it)) {
+            const int r = it.r0 + row;
+            const long long gr = (long long)it.bh * rows + r, gs = (long long)it.bh * a.stat_stride + r;
+            const float ndelta = !kDkv && r < rows ? a.delta[gs] : 0.f;
+            const uint64_t nd = f32x2_pack(__float_as_uint(ndelta), __float_as_uint(ndelta));
+            for (int b = 0; b < it.n_blk; ++b) {
+                const int s = stage.i;
+                const uint32_t tS = tm + kBColS + 128 * buf.i + 64 * half + lane_base;
+                const int lim = it.cols - (it.b0 + b) * kXCols - 64 * half;  // of this half's columns, those visible
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars.sfull[buf.i], buf.phase, abort) &&
+                                                 mbar_wait(&bars.pfull, pphase, abort));
+                if (!ok) break;
+                tc_fence_after();
+                if constexpr (kDkv) {
+                    // the block's -D and 1 / l (zeros past the last query)
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars.full[s], stage.phase, abort));
+                    if (!ok) break;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[32], g[32];
+                    tmem_ld32(tP + 32 * h, g);
+                    tmem_ld32(tS + 32 * h, v);
+                    tmem_ld_wait();
+                    if (h == 1) {  // P is read: the next step's may be formed
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars.pfree);
+                    }
+                    if constexpr (kDkv) {
+                        const float2 *sd = reinterpret_cast<const float2 *>(sm_stat + s * kBStat) + 32 * half + 16 * h;
+                        const float2 *sr = sd + 64;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            uint32_t w[8], e[8];
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) {
+                                const int c = 16 * u + 2 * y;
+                                const float2 fd = sd[c / 2], fr = sr[c / 2];
+                                const uint64_t s2 = f32x2_pack(v[c], v[c + 1]), g2 = f32x2_pack(g[c], g[c + 1]);
+                                const uint64_t d2 = f32x2_pack(__float_as_uint(fd.x), __float_as_uint(fd.y));
+                                const uint64_t r2 = f32x2_pack(__float_as_uint(fr.x), __float_as_uint(fr.y));
+                                const uint64_t sr2 = f32x2_mul(s2, r2);
+                                w[y] = f32x2_to_bf16x2(f32x2_mul(s2, sr2));
+                                e[y] = f32x2_to_bf16x2(f32x2_mul(sr2, f32x2_add(g2, d2)));  // ds / 2
+                            }
+                            tmem_st8(tS + 32 * h + 8 * u, w);
+                            tmem_st8(tS + 32 * h + 16 + 8 * u, e);
+                        }
+                    } else {
+                        if (lim < 64) {
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) {
+                                v[y] = 32 * h + y < lim ? v[y] : 0u;
+                                g[y] = 32 * h + y < lim ? g[y] : 0u;
+                            }
+                        }
+                        uint32_t w[16];
+#pragma unroll
+                        for (int y = 0; y < 16; ++y)
+                            w[y] = f32x2_to_bf16x2(f32x2_mul(f32x2_pack(v[2 * y], v[2 * y + 1]),
+                                                             f32x2_add(f32x2_pack(g[2 * y], g[2 * y + 1]), nd)));
+                        tmem_st16(tS + 32 * h, w);
+                    }
+                }
+                // dq: keys past the visible ones may be anything (NaN times a zero weight is
+                // NaN): cleared in the block where the visible keys end
+                if (!kDkv && lim < 64) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars.full[s], stage.phase, abort));
+                    if (!ok) break;
+                    uint8_t *op = sm_ring + s * kBStage + 64 * half * 128;
+                    for (int k = max(lim, 0) + qd; k < 64; k += 4)
+                        *reinterpret_cast<uint32_t *>(op + k * 128 + lane * 4) = 0u;
+                    fence_proxy_async_smem();
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    // the accumulating warps read the stage without waiting for it
+                    ok = kDkv || mbar_wait(&bars.full[s], stage.phase, abort);
+                    if (ok) mbar_arrive(&bars.wfull[buf.i]);
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                pphase ^= 1;
+                buf.next(2);
+                stage.next(kBStages);
+            }
+            if (!ok) break;
+            // dq: this half's 32 columns of the item's accumulator; dkv: half 0 dV, half 1 dK
+            constexpr int N = kDkv ? 64 : 32;
+            const int ob = kDkv ? half : acc.i;
+            uint32_t o[64];
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars.ofull[ob], kDkv ? ophase : acc.phase, abort));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tO = tm + 64 * ob + (kDkv ? 0 : 32 * half) + lane_base;
+            tmem_ld32(tO, o);
+            if (kDkv) tmem_ld32(tO + 32, o + 32);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.ofree[ob]);
+            if (kDkv && r >= it.live) {  // keys past the visible ones, whatever they hold
+#pragma unroll
+                for (int c = 0; c < N; ++c) o[c] = 0u;
+            }
+            const int c0 = kDkv ? 0 : 32 * half;  // first column held
+            if (r < rows && c0 < a.d) {
+                const int nc = min(N, a.d - c0);
+                if (it.part >= 0) {  // cut item: the row of the piece's slot (dkv: dv's rows, then dk's)
+                    const long long pr = x_part_row(a.sched, it.part) + row + (kDkv ? kXTile * half : 0);
+                    store_part(a.part + pr * a.d + c0, o, nc);
+                } else {
+                    const float f = !kDkv ? 2.f * a.rden[gs] : half ? 2.f : 1.f;
+                    store_row((kDkv && half ? a.o1 : a.o0) + gr * a.d + c0, nullptr, o, f, nc);
+                }
+            }
+            __syncwarp();
+            ophase ^= 1;
+            acc.next(2);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kBS) tmem_dealloc(tm, 512);
+    if (tid == 0 && abort_flag) atomicCAS(a.status, 0, (int)KATA_ERR_TIMEOUT);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    XLaunch x;
+    cudaError_t e = x_launch(static_cast<CrossMode>(MODE), p, io, x);
+    if (e != cudaSuccess) return e;
+    if ((e = smem_opt_in_once<cross_bwd_kernel<MODE>>(kBSmem)) != cudaSuccess) return e;
+    ProfScope prof(MODE == kCrossDq ? "cross_dq" : "cross_dkv", st);
+    cross_bwd_kernel<MODE>
+        <<<x.a.sched.grid, kBThreads, kBSmem, st>>>(x.maps[0], x.maps[1], x.maps[2], x.maps[3], x.a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cross_bwd_tc(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    return mode == kCrossDq ? launch_mode<kCrossDq>(p, io, st) : launch_mode<kCrossDkv>(p, io, st);
+}
+
+}  // namespace kata

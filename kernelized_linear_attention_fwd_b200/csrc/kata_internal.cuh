@@ -229,7 +229,7 @@ struct CrossPlan {
     kata_dtype dtype;
     long long BH;
     int R;             // rows per problem
-    int R_pad;         // R rounded up to 64: row stride of the statistics
+    int R_pad;         // R rounded up to 128: row stride of the statistics
     int splits[3];     // fp32, per CrossMode: pieces of the summed axis (1: no join)
     XSched sched[3];   // bf16, per CrossMode
     // workspace (bytes)
@@ -250,7 +250,8 @@ struct CrossIo {
 cudaError_t launch_cross_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 cudaError_t launch_cross_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 // One mode's main kernel: bf16 on the tensor cores, fp32 on the CUDA cores.
-cudaError_t launch_cross_tc(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
+cudaError_t launch_cross_fwd_tc(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
+cudaError_t launch_cross_bwd_tc(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 cudaError_t launch_cross_simt(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 // Rows per CTA of the fp32 kernels.
 int cross_simt_rows(CrossMode mode, const CrossPlan &p);

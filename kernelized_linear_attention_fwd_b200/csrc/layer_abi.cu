@@ -162,7 +162,7 @@ int cross_splits(long long items, long long steps, int min_steps) {
 // that its start and the join cost more than the steps it saves.
 bool cross_sched(const CrossPlan &p, CrossMode m, int rows, int cols, XSched &s) {
     const long long tiles = (rows + 127) / 128, tpi = cross_tc_tiles(m);
-    const long long blocks = (cols + cross_tc_cols(m) - 1) / cross_tc_cols(m);
+    const long long blocks = (cols + kXCols - 1) / kXCols;
     const long long items = p.BH * ((tiles + tpi - 1) / tpi);
     if (items >= (1LL << 31) || p.BH > (1LL << 62) / tiles / blocks) return false;
     const long long units = p.BH * tiles * blocks;
@@ -178,7 +178,8 @@ bool cross_sched(const CrossPlan &p, CrossMode m, int rows, int cols, XSched &s)
     const long long most = s.whole ? items : (units + s.min_share - 1) / s.min_share;
     s.grid = (int)(most < kPlanSms ? most : kPlanSms);
     if (s.whole) s.min_share = 1;
-    s.slot_rows = m == kCrossDkv ? 256 : rows < 256 ? rows : 256;  // dkv: dv's 128 rows and dk's
+    const int most_rows = m == kCrossDq ? 128 : 256;  // forward: two tiles; dkv: dv's 128 rows and dk's
+    s.slot_rows = m != kCrossDkv && rows < most_rows ? rows : most_rows;
     return true;
 }
 
@@ -198,7 +199,7 @@ kata_status cross_plan(int B, int H, int Hkv, int Tq, int Tk, int d, kata_dtype 
     p.BH = (long long)B * Hkv;
     if (p.BH > (1LL << 40) / rows || p.BH > (1LL << 40) / Tk) return KATA_ERR_UNSUPPORTED;
     p.R = (int)rows;
-    p.R_pad = (p.R + 63) / 64 * 64;
+    p.R_pad = (p.R + 127) / 128 * 128;
     const size_t stat = align_up((size_t)p.BH * p.R_pad * 4);
     p.ws_delta = 0;
     p.ws_rden = stat;
