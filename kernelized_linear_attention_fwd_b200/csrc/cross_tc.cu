@@ -229,7 +229,8 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                 if (!ok) break;
                                 ophase ^= 1;
                             }
-                            ok = mbar_wait(&bars.pfull[me][buf.i], (pphase >> buf.i) & 1, abort);
+                            ok = mbar_wait(&bars.full[stage.i], stage.phase, abort) &&
+                                 mbar_wait(&bars.pfull[me][buf.i], (pphase >> buf.i) & 1, abort);
                             if (!ok) break;
                             pphase ^= 1u << buf.i;
                             tc_fence_after();
@@ -258,7 +259,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         int j = 0, ns = 0, n = 0;
         uint32_t uses = 0, sphase = 0;  // sphase: parity of this half's next use of each buffer
         bool ok = true;
-        zero_dead_rows<kCrossFwd>(a, warp, lane);
+        zero_dead_rows<kCrossFwd>(a, warp, 8, lane);
         __syncwarp();
         while (ok && iter.next(it)) {
             // the tile this half takes, if any
@@ -311,12 +312,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    // the accumulating warps read the stage without waiting for it
-                    ok = mbar_wait(&bars.full[s], fpar, abort);
-                    if (ok) mbar_arrive(&bars.pfull[half][x]);
-                }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (lane == 0) mbar_arrive(&bars.pfull[half][x]);
             }
             if (!ok) break;
             if (t >= 0) {

@@ -6,23 +6,27 @@
 // weights, and one (dq) or two (dkv) products accumulate.  Tensor memory holds
 //
 //   0 .. 127    accumulators: dq: two of 64 columns, items in turn; dkv: dV, dK
-//   128, 256    S of even and odd steps; the weights replace it, per 32 scores the
-//               16 columns of ds (dq) or of w / l and ds (dkv)
+//   128, 256    S of even and odd steps; the weights replace it: per 16 scores 8
+//               columns of ds (dq) or of w / l and 8 of ds (dkv)
 //   384         P, free again once the warps have read it
 //
 // so the next step's S is formed while this step's scores are turned, its P right
 // after them, and a step's accumulation overlaps the next one's scores.  128-column
 // score products run at the full rate (N = 64 ones pay for reading the 128-row
 // operand twice as often: a 64-column form of these kernels took 1.6 times as long).
-// Warp 8 loads, warp 9 issues S, warp 10 issues P, warps 11 and 12 accumulate (dq:
-// 11 only).  Warps 0-3 turn columns 0 .. 63 of a step, warps 4-7 columns 64 .. 127.
+// One warp loads, one issues S, one P, two accumulate (dq: one).  16 warps turn
+// scores into weights, 32 columns each of their 32 rows: with 8 warps of 64 columns
+// their latency, not their instruction count, set the step (dkv: 1750 cycles of a
+// 2300-cycle step).
 #include "cross_tc.cuh"
 
 namespace kata {
 namespace {
 
-constexpr int kBThreads = 416;
-constexpr int kBTma = 8, kBS = 9, kBP = 10, kBAcc = 11;
+constexpr int kBGroups = 4;  // groups of 4 warps that turn scores into weights
+constexpr int kBThreads = 32 * (4 * kBGroups + 5);
+constexpr int kBTma = 4 * kBGroups, kBS = kBTma + 1, kBP = kBTma + 2, kBAcc = kBTma + 3;
+constexpr int kBCols = kXCols / kBGroups;  // columns of a step that a group turns
 constexpr int kBSlot = 2 * 16384;    // an item's two row operands
 constexpr int kBOp = kXCols * 128;   // one column operand of a block
 constexpr int kBStage = 2 * kBOp;
@@ -61,10 +65,10 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constan
             mbar_init(&bars.qfull[i], 1);
             mbar_init(&bars.qempty[i], 2);  // both score warps
             mbar_init(&bars.sfull[i], 1);
-            mbar_init(&bars.wfull[i], 8);
+            mbar_init(&bars.wfull[i], 4 * kBGroups);
             mbar_init(&bars.sfree[i], kDkv ? 2 : 1);
             mbar_init(&bars.ofull[i], 1);
-            mbar_init(&bars.ofree[i], kDkv ? 4 : 8);
+            mbar_init(&bars.ofree[i], 4 * kBGroups / (kDkv ? 2 : 1));
         }
         for (int i = 0; i < 4; ++i) mbar_init(&bars.drain[i], 1);
         for (int i = 0; i < kBStages; ++i) {
@@ -72,7 +76,7 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constan
             mbar_init(&bars.empty[i], 1);
         }
         mbar_init(&bars.pfull, 1);
-        mbar_init(&bars.pfree, 8);
+        mbar_init(&bars.pfree, 4 * kBGroups);
         fence_mbarrier_init();
     }
     if (warp == kBS) {
@@ -195,14 +199,14 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constan
                 ok = mbar_wait(&bars.ofree[o], kDkv ? ophase : acc.phase ^ 1, abort);
                 for (int b = 0; b < it.n_blk && ok; ++b) {
                     const uint64_t c = desc_at(dC, stage.i * kBStage);
-                    const uint32_t w = tm + kBColS + 128 * buf.i + 16 * me;
-                    ok = mbar_wait(&bars.wfull[buf.i], buf.phase, abort);
+                    const uint32_t w = tm + kBColS + 128 * buf.i + 8 * me;
+                    ok = mbar_wait(&bars.full[stage.i], stage.phase, abort) &&
+                         mbar_wait(&bars.wfull[buf.i], buf.phase, abort);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        mma_ts(tm + 64 * o, w + 32 * (ks / 2) + 8 * (ks % 2), desc_at(c, 2048 * ks), id,
-                               b > 0 || ks > 0);
+                        mma_ts(tm + 64 * o, w + 16 * ks, desc_at(c, 2048 * ks), id, b > 0 || ks > 0);
                     mma_commit(&bars.sfree[buf.i]);
                     buf.next(2);
                     stage.next(kBStages);
@@ -217,15 +221,15 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constan
         }
     } else {
         // ------------------------------------------------------------ weights and epilogue
-        const int half = warp / 4, qd = warp % 4;
+        const int grp = warp / 4, qd = warp % 4;
         const int row = 32 * qd + lane;
         const uint32_t lane_base = static_cast<uint32_t>(32 * qd) << 16;
         const int rows = a.sched.rows;
-        const uint32_t tP = tm + kBColP + 64 * half + lane_base;
+        const uint32_t tP = tm + kBColP + kBCols * grp + lane_base;
         XRing stage, buf, acc;
         uint32_t pphase = 0, ophase = 0;
         bool ok = true;
-        zero_dead_rows<MODE>(a, warp, lane);
+        zero_dead_rows<MODE>(a, warp, 4 * kBGroups, lane);
         __syncwarp();
         while (ok && iter.next(it)) {
             const int r = it.r0 + row;
@@ -234,99 +238,97 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constan
             const uint64_t nd = f32x2_pack(__float_as_uint(ndelta), __float_as_uint(ndelta));
             for (int b = 0; b < it.n_blk; ++b) {
                 const int s = stage.i;
-                const uint32_t tS = tm + kBColS + 128 * buf.i + 64 * half + lane_base;
-                const int lim = it.cols - (it.b0 + b) * kXCols - 64 * half;  // of this half's columns, those visible
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars.sfull[buf.i], buf.phase, abort) &&
-                                                 mbar_wait(&bars.pfull, pphase, abort));
-                if (!ok) break;
-                tc_fence_after();
+                const uint32_t tS = tm + kBColS + 128 * buf.i + kBCols * grp + lane_base;
+                // of this group's columns, those visible (dkv masks none)
+                const int lim = it.cols - (it.b0 + b) * kXCols - kBCols * grp;
                 if constexpr (kDkv) {
                     // the block's -D and 1 / l (zeros past the last query)
                     ok = __all_sync(0xffffffffu, mbar_wait(&bars.full[s], stage.phase, abort));
                     if (!ok) break;
                 }
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars.sfull[buf.i], buf.phase, abort) &&
+                                                 mbar_wait(&bars.pfull, pphase, abort));
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[32], g[32];
-                    tmem_ld32(tP + 32 * h, g);
-                    tmem_ld32(tS + 32 * h, v);
+                for (int h = 0; h < kBCols / 16; ++h) {
+                    uint32_t v[16], g[16], w[8];
+                    tmem_ld16(tP + 16 * h, g);
+                    tmem_ld16(tS + 16 * h, v);
                     tmem_ld_wait();
-                    if (h == 1) {  // P is read: the next step's may be formed
+                    if (h == kBCols / 16 - 1) {  // P is read: the next step's may be formed
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bars.pfree);
                     }
                     if constexpr (kDkv) {
-                        const float2 *sd = reinterpret_cast<const float2 *>(sm_stat + s * kBStat) + 32 * half + 16 * h;
-                        const float2 *sr = sd + 64;
+                        const float4 *sd =
+                            reinterpret_cast<const float4 *>(sm_stat + s * kBStat) + (kBCols * grp + 16 * h) / 4;
+                        const float4 *sr = sd + 32;
+                        uint32_t e[8];
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            uint32_t w[8], e[8];
+                        for (int y = 0; y < 4; ++y) {
+                            const float4 fd = sd[y], fr = sr[y];
 #pragma unroll
-                            for (int y = 0; y < 8; ++y) {
-                                const int c = 16 * u + 2 * y;
-                                const float2 fd = sd[c / 2], fr = sr[c / 2];
+                            for (int z = 0; z < 2; ++z) {
+                                const int c = 4 * y + 2 * z;
                                 const uint64_t s2 = f32x2_pack(v[c], v[c + 1]), g2 = f32x2_pack(g[c], g[c + 1]);
-                                const uint64_t d2 = f32x2_pack(__float_as_uint(fd.x), __float_as_uint(fd.y));
-                                const uint64_t r2 = f32x2_pack(__float_as_uint(fr.x), __float_as_uint(fr.y));
+                                const uint64_t d2 =
+                                    f32x2_pack(__float_as_uint(z ? fd.z : fd.x), __float_as_uint(z ? fd.w : fd.y));
+                                const uint64_t r2 =
+                                    f32x2_pack(__float_as_uint(z ? fr.z : fr.x), __float_as_uint(z ? fr.w : fr.y));
                                 const uint64_t sr2 = f32x2_mul(s2, r2);
-                                w[y] = f32x2_to_bf16x2(f32x2_mul(s2, sr2));
-                                e[y] = f32x2_to_bf16x2(f32x2_mul(sr2, f32x2_add(g2, d2)));  // ds / 2
+                                w[c / 2] = f32x2_to_bf16x2(f32x2_mul(s2, sr2));
+                                e[c / 2] = f32x2_to_bf16x2(f32x2_mul(sr2, f32x2_add(g2, d2)));  // ds / 2
                             }
-                            tmem_st8(tS + 32 * h + 8 * u, w);
-                            tmem_st8(tS + 32 * h + 16 + 8 * u, e);
                         }
+                        tmem_st8(tS + 16 * h, w);
+                        tmem_st8(tS + 16 * h + 8, e);
                     } else {
-                        if (lim < 64) {
+                        if (lim < kBCols) {
 #pragma unroll
-                            for (int y = 0; y < 32; ++y) {
-                                v[y] = 32 * h + y < lim ? v[y] : 0u;
-                                g[y] = 32 * h + y < lim ? g[y] : 0u;
+                            for (int y = 0; y < 16; ++y) {
+                                v[y] = 16 * h + y < lim ? v[y] : 0u;
+                                g[y] = 16 * h + y < lim ? g[y] : 0u;
                             }
                         }
-                        uint32_t w[16];
 #pragma unroll
-                        for (int y = 0; y < 16; ++y)
+                        for (int y = 0; y < 8; ++y)
                             w[y] = f32x2_to_bf16x2(f32x2_mul(f32x2_pack(v[2 * y], v[2 * y + 1]),
                                                              f32x2_add(f32x2_pack(g[2 * y], g[2 * y + 1]), nd)));
-                        tmem_st16(tS + 32 * h, w);
+                        tmem_st8(tS + 16 * h, w);
                     }
                 }
                 // dq: keys past the visible ones may be anything (NaN times a zero weight is
                 // NaN): cleared in the block where the visible keys end
-                if (!kDkv && lim < 64) {
+                if (!kDkv && lim < kBCols) {
                     ok = __all_sync(0xffffffffu, mbar_wait(&bars.full[s], stage.phase, abort));
                     if (!ok) break;
-                    uint8_t *op = sm_ring + s * kBStage + 64 * half * 128;
-                    for (int k = max(lim, 0) + qd; k < 64; k += 4)
+                    uint8_t *op = sm_ring + s * kBStage + kBCols * grp * 128;
+                    for (int k = max(lim, 0) + qd; k < kBCols; k += 4)
                         *reinterpret_cast<uint32_t *>(op + k * 128 + lane * 4) = 0u;
                     fence_proxy_async_smem();
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    // the accumulating warps read the stage without waiting for it
-                    ok = kDkv || mbar_wait(&bars.full[s], stage.phase, abort);
-                    if (ok) mbar_arrive(&bars.wfull[buf.i]);
-                }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
+                if (lane == 0) mbar_arrive(&bars.wfull[buf.i]);
                 pphase ^= 1;
                 buf.next(2);
                 stage.next(kBStages);
             }
             if (!ok) break;
-            // dq: this half's 32 columns of the item's accumulator; dkv: half 0 dV, half 1 dK
-            constexpr int N = kDkv ? 64 : 32;
-            const int ob = kDkv ? half : acc.i;
+            // this group's columns of the item's accumulators: dq: 64 / groups of them; dkv: the
+            // first groups dV's, the others dK's
+            constexpr int N = kDkv ? 128 / kBGroups : 64 / kBGroups;
+            const int ob = kDkv ? grp / (kBGroups / 2) : acc.i;
+            const int c0 = kDkv ? N * (grp % (kBGroups / 2)) : N * grp;
             uint32_t o[64];
             ok = __all_sync(0xffffffffu, mbar_wait(&bars.ofull[ob], kDkv ? ophase : acc.phase, abort));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t tO = tm + 64 * ob + (kDkv ? 0 : 32 * half) + lane_base;
-            tmem_ld32(tO, o);
-            if (kDkv) tmem_ld32(tO + 32, o + 32);
+#pragma unroll
+            for (int c = 0; c < N; c += 16) tmem_ld16(tm + 64 * ob + c0 + c + lane_base, o + c);
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
@@ -335,15 +337,14 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constan
 #pragma unroll
                 for (int c = 0; c < N; ++c) o[c] = 0u;
             }
-            const int c0 = kDkv ? 0 : 32 * half;  // first column held
             if (r < rows && c0 < a.d) {
                 const int nc = min(N, a.d - c0);
                 if (it.part >= 0) {  // cut item: the row of the piece's slot (dkv: dv's rows, then dk's)
-                    const long long pr = x_part_row(a.sched, it.part) + row + (kDkv ? kXTile * half : 0);
+                    const long long pr = x_part_row(a.sched, it.part) + row + (kDkv ? kXTile * ob : 0);
                     store_part(a.part + pr * a.d + c0, o, nc);
                 } else {
-                    const float f = !kDkv ? 2.f * a.rden[gs] : half ? 2.f : 1.f;
-                    store_row((kDkv && half ? a.o1 : a.o0) + gr * a.d + c0, nullptr, o, f, nc);
+                    const float f = !kDkv ? 2.f * a.rden[gs] : ob ? 2.f : 1.f;
+                    store_row((kDkv && ob ? a.o1 : a.o0) + gr * a.d + c0, nullptr, o, f, nc);
                 }
             }
             __syncwarp();
