@@ -5,6 +5,7 @@
 
 #include "cross_sched.cuh"
 #include "kata_internal.cuh"
+#include "sm100.cuh"
 
 namespace kata {
 namespace {
@@ -124,55 +125,43 @@ cudaError_t launch_join(const CrossPlan &p, CrossMode mode, const float *part, c
 // Joins the items that the tensor cores' schedule cut (cross_sched.cuh).  Grid x: the
 // stretch boundaries c = 1 .. G - 1; the block of the first boundary inside an item
 // adds the item's pieces in order: the end of CTA c - 1's stretch, then the starts
-// of the later CTAs' up to the item's end.  A block of 256 threads takes 16 / G16
-// rows (grid y), thread = 4 columns of a row and every G16-th piece.
+// of the later CTAs' up to the item's end, as the CTAs have recorded them.  A block
+// of 256 threads takes 16 / G16 rows (grid y), thread = 4 columns of a row and every
+// G16-th piece.
 template <int MODE, int G16>
 __global__ void __launch_bounds__(256)
-cross_tc_join_kernel(const XSched s, const float *part, const float *part_l, const float *rden, __nv_bfloat16 *o0,
-                     __nv_bfloat16 *o1, float *y, float *den, int grid, int R_pad, int d) {
-    constexpr int TPI = cross_tc_tiles(MODE), kRows = 16 / G16;
-    __shared__ long long sh[4];  // piece range, first slot, item
+cross_tc_join_kernel(const XSched s, const XPiece *pieces, const float *part, const float *part_l, const float *rden,
+                     __nv_bfloat16 *o0, __nv_bfloat16 *o1, float *y, float *den, int grid, int R_pad, int d) {
+    constexpr int kRows = 16 / G16;
     __shared__ float4 red[16][16];
     __shared__ float red_l[16];
-    const int c = blockIdx.x + 1;
-    if (threadIdx.x < 32) {
-        const XLine<MODE> line(s, threadIdx.x);
-        const long long n = line.share(s, grid), u = n * c;
-        long long seq0;
-        const XPos at = line.place(s, u, seq0);
-        if (threadIdx.x == 0) {
-            sh[0] = 0;
-            if (u < line.total && at.blk > 0) {
-                int live, tiles, blocks;
-                x_extent<MODE>(s, at.b, live, tiles, blocks);
-                const int nt = min(TPI, tiles - TPI * at.p);
-                const long long u0 = seq0 + (long long)at.h * tiles * blocks + (long long)at.p * TPI * blocks;
-                const long long u1 = u0 + (long long)nt * blocks;
-                // boundaries below u0 + nt are moved down to the item's start
-                if ((u0 + nt + n - 1) / n == c) {
-                    sh[0] = (u1 - 1) / n - c + 2;                          // pieces
-                    sh[1] = 2 * (c - 1) + ((long long)(c - 1) * n >= u0 ? 0 : 1);  // the first one's slot
-                    sh[2] = (long long)at.b * s.Hkv + at.h;
-                    sh[3] = (long long)at.p * TPI * 128;
-                }
+    sm100::griddep_wait();
+    const int c = blockIdx.x + 1, lane = threadIdx.x % 32;
+    const XPiece me = pieces[c], prev = pieces[c - 1];
+    const bool same = prev.bh == me.bh && prev.r0 == me.r0;
+    if (me.bh < 0 || !me.cont || (same && prev.cont)) return;
+    const int slot0 = 2 * (c - 1) + (same ? 0 : 1);  // the item began that CTA's stretch, or ended it
+    int n = 2;                                       // pieces
+    if (!me.last)
+        for (int x = c + 1;; x += 32) {  // up to the CTA that reaches the item's end
+            const bool end = x + lane >= grid || pieces[x + lane].last;
+            const unsigned m = __ballot_sync(0xffffffffu, end);
+            if (m) {
+                n = x + __ffs(m) - c + 1;
+                break;
             }
         }
-    }
-    __syncthreads();
-    const int pieces = (int)sh[0];
-    if (pieces == 0) return;
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, g = ty % G16, col = 4 * tx;
     const int row = blockIdx.y * kRows + ty / G16;  // of the slot
     // dkv: rows 0 .. 127 of a slot are dv's, the others dk's
-    const int r = (int)sh[3] + (MODE == kCrossDkv ? row % 128 : row);
-    const bool on = r < s.rows && row < TPI * 128 * (MODE == kCrossDkv ? 2 : 1) && col < d;
+    const int r = me.r0 + (MODE == kCrossDkv ? row % 128 : row);
+    const bool on = r < s.rows && row < s.slot_rows && col < d;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
     if (on) {
 #pragma unroll 4
-        for (int x = g; x < pieces; x += G16) {
-            const long long slot = x == 0 ? sh[1] : 2LL * (c - 1 + x);
-            const long long pr = slot * s.slot_rows + row;
+        for (int x = g; x < n; x += G16) {
+            const long long pr = (x == 0 ? slot0 : 2LL * (c - 1 + x)) * s.slot_rows + row;
             const float4 w = *reinterpret_cast<const float4 *>(part + pr * d + col);
             v.x += w.x;
             v.y += w.y;
@@ -201,13 +190,13 @@ cross_tc_join_kernel(const XSched s, const float *part, const float *part_l, con
     if (!on) return;
     float f = 1.f;
     if (MODE == kCrossFwd) f = cross_recip(l);
-    if (MODE == kCrossDq) f = 2.f * rden[sh[2] * R_pad + r];
+    if (MODE == kCrossDq) f = 2.f * rden[(long long)me.bh * R_pad + r];
     if (MODE == kCrossDkv && row >= 128) f = 2.f;
     v.x *= f;
     v.y *= f;
     v.z *= f;
     v.w *= f;
-    const long long gr = sh[2] * s.rows + r, o = gr * d + col;
+    const long long gr = (long long)me.bh * s.rows + r, o = gr * d + col;
     __nv_bfloat16 *dst = MODE == kCrossDkv && row >= 128 ? o1 : o0;
     __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
     *reinterpret_cast<uint2 *>(dst + o) =
@@ -220,8 +209,7 @@ cross_tc_join_kernel(const XSched s, const float *part, const float *part_l, con
 
 template <int MODE>
 cudaError_t launch_tc_join(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
-    XSched s = p.sched[MODE];
-    s.key_lengths = io.key_lengths;
+    const XSched &s = p.sched[MODE];
     if (s.whole || s.grid == 1) return cudaSuccess;
     char *ws = static_cast<char *>(io.ws);
     const float *part = reinterpret_cast<const float *>(ws + p.ws_part[MODE]);
@@ -233,14 +221,10 @@ cudaError_t launch_tc_join(const CrossPlan &p, const CrossIo &io, cudaStream_t s
     // few rows: an item is cut into many pieces, which 16 threads share per 4 columns
     const bool few = s.slot_rows <= 64;
     const dim3 grid(s.grid - 1, few ? s.slot_rows : (s.slot_rows + 15) / 16);
+    const XPiece *pieces = reinterpret_cast<const XPiece *>(ws + p.ws_pieces[MODE]);
     ProfScope prof("cross_join", st);
-    if (few)
-        cross_tc_join_kernel<MODE, 16><<<grid, 256, 0, st>>>(s, part, part_l, rden, o0, o1, io.y, io.den, s.grid,
-                                                              p.R_pad, p.d);
-    else
-        cross_tc_join_kernel<MODE, 1><<<grid, 256, 0, st>>>(s, part, part_l, rden, o0, o1, io.y, io.den, s.grid,
-                                                             p.R_pad, p.d);
-    return cudaGetLastError();
+    return launch_dependent(few ? cross_tc_join_kernel<MODE, 16> : cross_tc_join_kernel<MODE, 1>, grid, 256u, 0, st, s,
+                            pieces, part, part_l, rden, o0, o1, io.y, io.den, s.grid, p.R_pad, p.d);
 }
 
 cudaError_t launch_main(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {

@@ -26,12 +26,19 @@ struct XPos {
 struct XRange {
     XPos from, to;
 };
+// What the join needs of a CTA's first piece (XIter::first): its item, whether it
+// continues one that an earlier CTA began, and whether it reaches the item's end.
+struct alignas(16) XPiece {
+    int bh, r0;
+    int cont, last;
+};
 // A stretch of blocks of one item.
 struct XItem {
     int bh, r0, n_tiles, b0, n_blk;
     int cols;  // columns in use (dkv: all of them)
     int live;  // visible keys of the sequence
     int part;  // slot of a cut item's piece, or -1
+    int reaches_end;
 };
 
 // T_b and N_b.
@@ -101,10 +108,9 @@ struct XLine {
         return n < s.min_share ? s.min_share : n;
     }
 
-    // Place of unit u; also the units before its sequence.
-    __device__ __forceinline__ XPos place(const XSched &s, long long u, long long &seq0) const {
+    // Place of unit u.
+    __device__ __forceinline__ XPos place(const XSched &s, long long u) const {
         XPos r = {s.B, 0, 0, 0};
-        seq0 = total;
         const bool mine = u < total && u >= before && u < before + units;
         if (mine) {
             long long at = before;
@@ -113,15 +119,13 @@ struct XLine {
                 x_extent<MODE>(s, 0, live, tiles, blocks);
                 const long long per = (long long)s.Hkv * tiles * blocks;
                 const int b = (int)(u / per);
-                seq0 = b * per;
-                r = x_place<MODE>(s, b, u - seq0, tiles, blocks);
+                r = x_place<MODE>(s, b, u - b * per, tiles, blocks);
             } else {
                 for (int b = first; b < last; ++b) {
                     int live, tiles, blocks;
                     x_extent<MODE>(s, b, live, tiles, blocks);
                     const long long per = (long long)s.Hkv * tiles * blocks;
                     if (u < at + per) {
-                        seq0 = at;
                         r = x_place<MODE>(s, b, u - at, tiles, blocks);
                         break;
                     }
@@ -135,7 +139,6 @@ struct XLine {
         r.h = __shfl_sync(0xffffffffu, r.h, src);
         r.p = __shfl_sync(0xffffffffu, r.p, src);
         r.blk = __shfl_sync(0xffffffffu, r.blk, src);
-        seq0 = __shfl_sync(0xffffffffu, seq0, src);
         return r;
     }
 };
@@ -145,10 +148,9 @@ template <int MODE>
 __device__ __forceinline__ XRange x_range(const XSched &s, int c, int grid, int lane) {
     const XLine<MODE> line(s, lane);
     const long long n = line.share(s, grid);
-    long long unused;
     XRange r;
-    r.from = line.place(s, n * c, unused);
-    r.to = line.place(s, n * (c + 1), unused);
+    r.from = line.place(s, n * c);
+    r.to = line.place(s, n * (c + 1));
     return r;
 }
 
@@ -159,6 +161,14 @@ struct XIter {
     int pieces = 0;
 
     __device__ __forceinline__ XIter(const XSched &s_, const XRange &r) : s(s_), at(r.from), to(r.to) {}
+
+    // The first piece, of an iterator that has not started (bh = -1: none).
+    __device__ __forceinline__ static XPiece first(const XSched &s, const XRange &r) {
+        XIter x(s, r);
+        XItem it;
+        if (!x.next(it)) return {-1, 0, 0, 0};
+        return {it.bh, it.r0, it.b0 > 0, it.reaches_end};
+    }
 
     __device__ __forceinline__ bool next(XItem &it) {
         constexpr int TPI = cross_tc_tiles(MODE);
@@ -179,6 +189,7 @@ struct XIter {
             it.n_blk = end - at.blk;
             it.cols = MODE == kCrossDkv ? s.cols : live;
             it.live = live;
+            it.reaches_end = end == blocks;
             it.part = at.blk == 0 && end == blocks ? -1 : 2 * (int)blockIdx.x + (pieces ? 1 : 0);
             ++pieces;
             if (cut) {

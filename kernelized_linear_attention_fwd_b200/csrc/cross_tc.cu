@@ -111,7 +111,10 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         __syncwarp();
         const XRange r = x_range<kCrossFwd>(a.sched, blockIdx.x, gridDim.x, lane);
-        if (lane == 0) range = r;
+        if (lane == 0) {
+            range = r;
+            if (!a.sched.whole) a.pieces[blockIdx.x] = XIter<kCrossFwd>::first(a.sched, r);
+        }
     }
     tc_fence_before();
     __syncthreads();

@@ -34,6 +34,7 @@ struct XArgs {
     __nv_bfloat16 *o0, *o1;  // forward: out; dq: dq; dkv: dv, dk
     float *y, *den;          // forward exports
     float *part, *part_l;    // partial sums of cut items
+    XPiece *pieces;          // every CTA's first piece
     const float *delta, *rden;
     int *status;
 };
@@ -125,6 +126,7 @@ inline cudaError_t x_launch(CrossMode mode, const CrossPlan &p, const CrossIo &i
     a.den = io.den;
     a.part = reinterpret_cast<float *>(ws + p.ws_part[mode]);
     a.part_l = reinterpret_cast<float *>(ws + p.ws_part_l);
+    a.pieces = reinterpret_cast<XPiece *>(ws + p.ws_pieces[mode]);
     a.delta = reinterpret_cast<const float *>(ws + p.ws_delta);
     a.rden = reinterpret_cast<const float *>(ws + p.ws_rden);
     a.status = device_status_ptr();

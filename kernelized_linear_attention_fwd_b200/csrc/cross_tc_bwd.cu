@@ -14,19 +14,23 @@
 // after them, and a step's accumulation overlaps the next one's scores.  128-column
 // score products run at the full rate (N = 64 ones pay for reading the 128-row
 // operand twice as often: a 64-column form of these kernels took 1.6 times as long).
-// One warp loads, one issues S, one P, two accumulate (dq: one).  16 warps turn
-// scores into weights, 32 columns each of their 32 rows: with 8 warps of 64 columns
-// their latency, not their instruction count, set the step (dkv: 1750 cycles of a
-// 2300-cycle step).
+// One warp loads, one issues S, one P, two accumulate (dq: one).  dkv has 16 warps
+// to turn scores into weights, 32 columns each of their 32 rows (8 warps of 64 columns
+// took 207 us where 16 take 189: 4 heads-batches of 16 heads, 2048 queries, 4096 keys,
+// ragged); dq, with half the arithmetic, has 8 (143 us; 16: 147).
 #include "cross_tc.cuh"
 
 namespace kata {
 namespace {
 
-constexpr int kBGroups = 4;  // groups of 4 warps that turn scores into weights
-constexpr int kBThreads = 32 * (4 * kBGroups + 5);
-constexpr int kBTma = 4 * kBGroups, kBS = kBTma + 1, kBP = kBTma + 2, kBAcc = kBTma + 3;
-constexpr int kBCols = kXCols / kBGroups;  // columns of a step that a group turns
+// Groups of 4 warps that turn scores into weights, and the other warps behind them.
+template <int MODE>
+struct BCfg {
+    static constexpr int kGroups = MODE == kCrossDq ? 2 : 4;
+    static constexpr int kThreads = 32 * (4 * kGroups + 5);
+    static constexpr int kTma = 4 * kGroups, kS = kTma + 1, kP = kTma + 2, kAcc = kTma + 3;
+    static constexpr int kCols = kXCols / kGroups;  // columns of a step that a group turns
+};
 constexpr int kBSlot = 2 * 16384;    // an item's two row operands
 constexpr int kBOp = kXCols * 128;   // one column operand of a block
 constexpr int kBStage = 2 * kBOp;
@@ -43,11 +47,14 @@ struct BBars {
 };
 
 template <int MODE>
-__global__ void __launch_bounds__(kBThreads, 1)
+__global__ void __launch_bounds__(BCfg<MODE>::kThreads, 1)
 cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant__ CUtensorMap tm_r1,
                  const __grid_constant__ CUtensorMap tm_c0, const __grid_constant__ CUtensorMap tm_c1,
                  const XArgs a) {
     constexpr bool kDkv = MODE == kCrossDkv;
+    using Cfg = BCfg<MODE>;
+    constexpr int kBGroups = Cfg::kGroups, kBCols = Cfg::kCols;
+    constexpr int kBTma = Cfg::kTma, kBS = Cfg::kS, kBP = Cfg::kP, kBAcc = Cfg::kAcc;
     extern __shared__ uint8_t smem_raw[];
     __shared__ BBars bars;
     __shared__ XRange range;
@@ -92,7 +99,10 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constan
         }
         __syncwarp();
         const XRange r = x_range<MODE>(a.sched, blockIdx.x, gridDim.x, lane);
-        if (lane == 0) range = r;
+        if (lane == 0) {
+            range = r;
+            if (!a.sched.whole) a.pieces[blockIdx.x] = XIter<MODE>::first(a.sched, r);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -250,41 +260,62 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constan
                                                  mbar_wait(&bars.pfull, pphase, abort));
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int h = 0; h < kBCols / 16; ++h) {
-                    uint32_t v[16], g[16], w[8];
-                    tmem_ld16(tP + 16 * h, g);
-                    tmem_ld16(tS + 16 * h, v);
+                if constexpr (kDkv) {
+                    // Fragment layout: -D and 1 / l of 8 queries serve the thread's 4 rows.  (One
+                    // row per thread would read all 32 columns' of each from shared memory.)
+                    static_assert(!kDkv || kBCols == 32, "fragment loads of 32 columns");
+                    const float2 *sd = reinterpret_cast<const float2 *>(sm_stat + s * kBStat) +
+                                       (kBCols * grp) / 2 + lane % 4;
+                    // P first, all of it: the next step's may then be formed under this one's arithmetic
+                    uint32_t g[32];
+                    tmem_ld_16x256b_x4(tP, g);
+                    tmem_ld_16x256b_x4(tP + (16u << 16), g + 16);
                     tmem_ld_wait();
-                    if (h == kBCols / 16 - 1) {  // P is read: the next step's may be formed
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars.pfree);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.pfree);
+                    float2 fd[4], fr[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        fd[j] = sd[4 * j];
+                        fr[j] = sd[64 + 4 * j];
                     }
-                    if constexpr (kDkv) {
-                        const float4 *sd =
-                            reinterpret_cast<const float4 *>(sm_stat + s * kBStat) + (kBCols * grp + 16 * h) / 4;
-                        const float4 *sr = sd + 32;
-                        uint32_t e[8];
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const float4 fd = sd[y], fr = sr[y];
+                    for (int u = 0; u < 2; ++u) {  // lanes 0 .. 15, 16 .. 31
+                        const uint32_t tSu = tS + (static_cast<uint32_t>(16 * u) << 16);
+                        uint32_t v[16];
+                        tmem_ld_16x256b_x4(tSu, v);
+                        tmem_ld_wait();
 #pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const int c = 4 * y + 2 * z;
-                                const uint64_t s2 = f32x2_pack(v[c], v[c + 1]), g2 = f32x2_pack(g[c], g[c + 1]);
-                                const uint64_t d2 =
-                                    f32x2_pack(__float_as_uint(z ? fd.z : fd.x), __float_as_uint(z ? fd.w : fd.y));
-                                const uint64_t r2 =
-                                    f32x2_pack(__float_as_uint(z ? fr.z : fr.x), __float_as_uint(z ? fr.w : fr.y));
+                        for (int h = 0; h < 2; ++h) {  // 16 columns: 8 of w / l, 8 of ds / 2
+                            uint32_t w[4], e[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const int j = 2 * h + y / 2, c = 8 * h + 2 * y;
+                                const uint64_t s2 = f32x2_pack(v[c], v[c + 1]);
+                                const uint64_t g2 = f32x2_pack(g[16 * u + c], g[16 * u + c + 1]);
+                                const uint64_t d2 = f32x2_pack(__float_as_uint(fd[j].x), __float_as_uint(fd[j].y));
+                                const uint64_t r2 = f32x2_pack(__float_as_uint(fr[j].x), __float_as_uint(fr[j].y));
                                 const uint64_t sr2 = f32x2_mul(s2, r2);
-                                w[c / 2] = f32x2_to_bf16x2(f32x2_mul(s2, sr2));
-                                e[c / 2] = f32x2_to_bf16x2(f32x2_mul(sr2, f32x2_add(g2, d2)));  // ds / 2
+                                w[y] = f32x2_to_bf16x2(f32x2_mul(s2, sr2));
+                                e[y] = f32x2_to_bf16x2(f32x2_mul(sr2, f32x2_add(g2, d2)));
                             }
+                            tmem_st_16x128b_x2(tSu + 16 * h, w);
+                            tmem_st_16x128b_x2(tSu + 16 * h + 8, e);
                         }
-                        tmem_st8(tS + 16 * h, w);
-                        tmem_st8(tS + 16 * h + 8, e);
-                    } else {
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < kBCols / 16; ++h) {
+                        uint32_t v[16], g[16], w[8];
+                        tmem_ld16(tP + 16 * h, g);
+                        tmem_ld16(tS + 16 * h, v);
+                        tmem_ld_wait();
+                        if (h == kBCols / 16 - 1) {  // P is read: the next step's may be formed
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bars.pfree);
+                        }
                         if (lim < kBCols) {
 #pragma unroll
                             for (int y = 0; y < 16; ++y) {
@@ -367,7 +398,7 @@ cudaError_t launch_mode(const CrossPlan &p, const CrossIo &io, cudaStream_t st) 
     if ((e = smem_opt_in_once<cross_bwd_kernel<MODE>>(kBSmem)) != cudaSuccess) return e;
     ProfScope prof(MODE == kCrossDq ? "cross_dq" : "cross_dkv", st);
     cross_bwd_kernel<MODE>
-        <<<x.a.sched.grid, kBThreads, kBSmem, st>>>(x.maps[0], x.maps[1], x.maps[2], x.maps[3], x.a);
+        <<<x.a.sched.grid, BCfg<MODE>::kThreads, kBSmem, st>>>(x.maps[0], x.maps[1], x.maps[2], x.maps[3], x.a);
     return cudaGetLastError();
 }
 

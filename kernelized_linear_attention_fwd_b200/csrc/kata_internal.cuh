@@ -144,6 +144,25 @@ cudaError_t smem_opt_in_once(int bytes) {
     return e;
 }
 
+// Launches `kernel` as a programmatic dependent of the call's previous kernel: its
+// launch overlaps that kernel's end, and it must execute griddepcontrol.wait before
+// it reads or writes what earlier work touches.
+template <typename... Exp, typename... Act>
+cudaError_t launch_dependent(void (*kernel)(Exp...), dim3 grid, unsigned block, int smem, cudaStream_t st,
+                             Act... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Exp>(args)...);
+}
+
 // Element loads as fp32.
 __device__ __forceinline__ float load_f32(const float *p, long long i) { return p[i]; }
 __device__ __forceinline__ float load_f32(const __nv_bfloat16 *p, long long i) {
@@ -235,6 +254,7 @@ struct CrossPlan {
     // workspace (bytes)
     size_t ws_part[3];  // partial sums of each mode
     size_t ws_part_l;   // forward: partial denominators
+    size_t ws_pieces[3];  // bf16: every CTA's first piece
     size_t ws_delta;    // backward: [BH][R_pad] -(dy.y), then [BH][R_pad] 1 / den
     size_t ws_rden;
     size_t ws_fwd_bytes, ws_bwd_bytes;

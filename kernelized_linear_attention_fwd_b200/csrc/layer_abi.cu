@@ -219,13 +219,16 @@ kata_status cross_plan(int B, int H, int Hkv, int Tq, int Tk, int d, kata_dtype 
             if (p.splits[m] > 1) part_rows = (size_t)p.splits[m] * p.BH * n * (m == kCrossDkv ? 2 : 1);
         }
         const size_t part = align_up(part_rows * d * 4);
+        const size_t pieces = dtype == KATA_BF16 && part ? align_up(p.sched[m].grid * sizeof(XPiece)) : 0;
         if (m == kCrossFwd) {
             p.ws_part[m] = 0;
             p.ws_part_l = part;
-            p.ws_fwd_bytes = part + align_up(part_rows * 4);
+            p.ws_pieces[m] = part + align_up(part_rows * 4);
+            p.ws_fwd_bytes = p.ws_pieces[m] + pieces;
         } else {
             p.ws_part[m] = off;
-            off += part;
+            p.ws_pieces[m] = off + part;
+            off += part + pieces;
         }
     }
     p.ws_bwd_bytes = off;

@@ -274,6 +274,28 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
         : "memory");
 }
 
+// 16 lanes x 32 consecutive 32-bit columns, fragment layout: thread t holds, per 8
+// columns j, columns 8 j + 2 (t % 4) and the next of lane t / 4 (r[4 j], r[4 j + 1])
+// and of lane t / 4 + 8 (r[4 j + 2], r[4 j + 3]).  A thread thus meets a quarter of
+// the columns, each in two lanes, where values per column are needed.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// 16 lanes x 8 consecutive 32-bit columns: thread t holds, per 4 columns j, column
+// 4 j + t % 4 of lane t / 4 (r[2 j]) and of lane t / 4 + 8 (r[2 j + 1]): the bf16
+// pairs of the load above.
+__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // Descriptors
 // ---------------------------------------------------------------------------
