@@ -12,32 +12,46 @@ namespace {
 
 // Row statistics of the backward pass: delta = -dy.y (y the forward's unrounded
 // output) and 1 / den (0 for a row without weight), zeros in the padding up to
-// R_pad.  8 lanes per row.
+// R_pad.
+__device__ __forceinline__ float dot8(const float *a, const float4 &x, const float4 &y) {
+    const float4 u = *reinterpret_cast<const float4 *>(a), v = *reinterpret_cast<const float4 *>(a + 4);
+    float s = u.x * x.x;
+    s = fmaf(u.y, x.y, s);
+    s = fmaf(u.z, x.z, s);
+    s = fmaf(u.w, x.w, s);
+    s = fmaf(v.x, y.x, s);
+    s = fmaf(v.y, y.y, s);
+    s = fmaf(v.z, y.z, s);
+    return fmaf(v.w, y.w, s);
+}
+__device__ __forceinline__ float dot8(const __nv_bfloat16 *a, const float4 &x, const float4 &y) {
+    const uint4 w = *reinterpret_cast<const uint4 *>(a);
+    const float u[8] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                        __uint_as_float(w.y & 0xFFFF0000u), __uint_as_float(w.z << 16),
+                        __uint_as_float(w.z & 0xFFFF0000u), __uint_as_float(w.w << 16),
+                        __uint_as_float(w.w & 0xFFFF0000u)};
+    return dot8(u, x, y);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256)
 cross_stats_kernel(const T *dout, const float *y, const float *den, float *delta, float *rden, long long BH, int R,
                    int R_pad, int d) {
-    const long long n = BH * R_pad;
-    const int sub = threadIdx.x % 8;
-    for (long long x = ((long long)blockIdx.x * 256 + threadIdx.x) / 8; x < n; x += (long long)gridDim.x * 32) {
-        const long long bh = x / R_pad;
+    const int lanes = d / 8, sub = threadIdx.x % lanes, per = 256 / lanes;  // 8 columns a lane
+    const long long n = BH * R_pad, rows = (n + per - 1) / per;
+    sm100::griddep_launch_dependents();
+    for (long long b = blockIdx.x; b < rows; b += gridDim.x) {  // every warp whole, for the shuffles
+        const long long x = b * per + threadIdx.x / lanes, bh = x / R_pad;
         const int r = (int)(x - bh * R_pad);
         float s = 0.f, rd = 0.f;
-        if (r < R) {
-            const long long row = bh * R + r;
-            for (int c = 4 * sub; c < d; c += 32) {
-                const float4 v = *reinterpret_cast<const float4 *>(y + row * d + c);
-                s = fmaf(load_f32(dout, row * d + c), v.x, s);
-                s = fmaf(load_f32(dout, row * d + c + 1), v.y, s);
-                s = fmaf(load_f32(dout, row * d + c + 2), v.z, s);
-                s = fmaf(load_f32(dout, row * d + c + 3), v.w, s);
-            }
-            rd = cross_recip(den[row]);
+        if (x < n && r < R) {
+            const long long o = (bh * R + r) * d + 8 * sub;
+            const float4 *yy = reinterpret_cast<const float4 *>(y + o);
+            s = dot8(dout + o, yy[0], yy[1]);
+            rd = cross_recip(den[bh * R + r]);
         }
-        // the 8 lanes of a row run the loop together
-        const unsigned mask = 0xffu << (threadIdx.x % 32 / 8 * 8);
-        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(mask, s, o);
-        if (sub == 0) {
+        for (int l = lanes / 2; l > 0; l >>= 1) s += __shfl_xor_sync(0xffffffffu, s, l);
+        if (sub == 0 && x < n) {
             delta[x] = -s;
             rden[x] = rd;
         }
@@ -122,16 +136,16 @@ cudaError_t launch_join(const CrossPlan &p, CrossMode mode, const float *part, c
     return cudaGetLastError();
 }
 
-// Joins the items that the tensor cores' schedule cut (cross_sched.cuh).  Grid x: the
+// Joins the items that the schedule of the tensor cores and of few rows cut (cross_sched.cuh).  Grid x: the
 // stretch boundaries c = 1 .. G - 1; the block of the first boundary inside an item
 // adds the item's pieces in order: the end of CTA c - 1's stretch, then the starts
 // of the later CTAs' up to the item's end, as the CTAs have recorded them.  A block
 // of 256 threads takes 16 / G16 rows (grid y), thread = 4 columns of a row and every
 // G16-th piece.
-template <int MODE, int G16>
+template <typename T, int MODE, int G16>
 __global__ void __launch_bounds__(256)
-cross_tc_join_kernel(const XSched s, const XPiece *pieces, const float *part, const float *part_l, const float *rden,
-                     __nv_bfloat16 *o0, __nv_bfloat16 *o1, float *y, float *den, int grid, int R_pad, int d) {
+cross_cut_join_kernel(const XSched s, const XPiece *pieces, const float *part, const float *part_l, const float *rden,
+                     T *o0, T *o1, float *y, float *den, int grid, int R_pad, int d) {
     constexpr int kRows = 16 / G16;
     __shared__ float4 red[16][16];
     __shared__ float red_l[16];
@@ -197,37 +211,38 @@ cross_tc_join_kernel(const XSched s, const XPiece *pieces, const float *part, co
     v.z *= f;
     v.w *= f;
     const long long gr = (long long)me.bh * s.rows + r, o = gr * d + col;
-    __nv_bfloat16 *dst = MODE == kCrossDkv && row >= 128 ? o1 : o0;
-    __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2 *>(dst + o) =
-        make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
+    T *dst = MODE == kCrossDkv && row >= 128 ? o1 : o0;
+    store_out(dst, o, v.x);
+    store_out(dst, o + 1, v.y);
+    store_out(dst, o + 2, v.z);
+    store_out(dst, o + 3, v.w);
     if (MODE == kCrossFwd) {
         if (y) *reinterpret_cast<float4 *>(y + o) = v;
         if (den && col == 0) den[gr] = l;
     }
 }
 
-template <int MODE>
-cudaError_t launch_tc_join(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+template <typename T, int MODE>
+cudaError_t launch_cut_join(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     const XSched &s = p.sched[MODE];
-    if (s.whole || s.grid == 1) return cudaSuccess;
+    if (cross_whole(s, io) || s.grid == 1) return cudaSuccess;
     char *ws = static_cast<char *>(io.ws);
     const float *part = reinterpret_cast<const float *>(ws + p.ws_part[MODE]);
     const float *part_l = reinterpret_cast<const float *>(ws + p.ws_part_l);
     const float *rden = reinterpret_cast<const float *>(ws + p.ws_rden);
-    __nv_bfloat16 *o0 =
-        static_cast<__nv_bfloat16 *>(MODE == kCrossFwd ? io.out : MODE == kCrossDq ? io.dq : io.dv);
-    __nv_bfloat16 *o1 = static_cast<__nv_bfloat16 *>(io.dk);
+    T *o0 = static_cast<T *>(MODE == kCrossFwd ? io.out : MODE == kCrossDq ? io.dq : io.dv);
+    T *o1 = static_cast<T *>(io.dk);
     // few rows: an item is cut into many pieces, which 16 threads share per 4 columns
     const bool few = s.slot_rows <= 64;
     const dim3 grid(s.grid - 1, few ? s.slot_rows : (s.slot_rows + 15) / 16);
     const XPiece *pieces = reinterpret_cast<const XPiece *>(ws + p.ws_pieces[MODE]);
     ProfScope prof("cross_join", st);
-    return launch_dependent(few ? cross_tc_join_kernel<MODE, 16> : cross_tc_join_kernel<MODE, 1>, grid, 256u, 0, st, s,
+    return launch_dependent(few ? cross_cut_join_kernel<T, MODE, 16> : cross_cut_join_kernel<T, MODE, 1>, grid, 256u, 0, st, s,
                             pieces, part, part_l, rden, o0, o1, io.y, io.den, s.grid, p.R_pad, p.d);
 }
 
 cudaError_t launch_main(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    if (mode == kCrossFwd && p.few) return launch_cross_few(p, io, st);
     if (p.dtype != KATA_BF16) return launch_cross_simt(mode, p, io, st);
     return mode == kCrossFwd ? launch_cross_fwd_tc(p, io, st) : launch_cross_bwd_tc(mode, p, io, st);
 }
@@ -235,7 +250,7 @@ cudaError_t launch_main(CrossMode mode, const CrossPlan &p, const CrossIo &io, c
 template <typename T>
 cudaError_t forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     cudaError_t e = launch_main(kCrossFwd, p, io, st);
-    if (e == cudaSuccess && p.dtype == KATA_BF16) return launch_tc_join<kCrossFwd>(p, io, st);
+    if (e == cudaSuccess && (p.few || p.dtype == KATA_BF16)) return launch_cut_join<T, kCrossFwd>(p, io, st);
     if (e != cudaSuccess || p.splits[kCrossFwd] == 1) return e;
     const char *ws = static_cast<const char *>(io.ws);
     return launch_join<T, kJoinDen>(p, kCrossFwd, reinterpret_cast<const float *>(ws + p.ws_part[kCrossFwd]),
@@ -249,7 +264,7 @@ cudaError_t backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     float *delta = reinterpret_cast<float *>(ws + p.ws_delta), *rden = reinterpret_cast<float *>(ws + p.ws_rden);
     {
         ProfScope prof("cross_stats", st);
-        const long long blocks = (p.BH * p.R_pad + 31) / 32, most = 8LL * kPlanSms;
+        const long long per = 256 / (p.d / 8), blocks = (p.BH * p.R_pad + per - 1) / per, most = 16LL * kPlanSms;
         cross_stats_kernel<T><<<(unsigned)(blocks < most ? blocks : most), 256, 0, st>>>(
             static_cast<const T *>(io.dout), io.y, io.den, delta, rden, p.BH, p.R, p.R_pad, p.d);
     }
@@ -257,9 +272,9 @@ cudaError_t backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if ((e = launch_main(kCrossDq, p, io, st)) != cudaSuccess) return e;
     if (p.dtype == KATA_BF16) {
-        if ((e = launch_tc_join<kCrossDq>(p, io, st)) != cudaSuccess) return e;
+        if ((e = launch_cut_join<T, kCrossDq>(p, io, st)) != cudaSuccess) return e;
         if ((e = launch_main(kCrossDkv, p, io, st)) != cudaSuccess) return e;
-        return launch_tc_join<kCrossDkv>(p, io, st);
+        return launch_cut_join<T, kCrossDkv>(p, io, st);
     }
     if (p.splits[kCrossDq] > 1) {
         e = launch_join<T, kJoinRow>(p, kCrossDq, reinterpret_cast<const float *>(ws + p.ws_part[kCrossDq]), nullptr,

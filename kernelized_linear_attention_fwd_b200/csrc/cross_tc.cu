@@ -111,14 +111,12 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         __syncwarp();
         const XRange r = x_range<kCrossFwd>(a.sched, blockIdx.x, gridDim.x, lane);
-        if (lane == 0) {
-            range = r;
-            if (!a.sched.whole) a.pieces[blockIdx.x] = XIter<kCrossFwd>::first(a.sched, r);
-        }
+        if (lane == 0) range = r;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    griddep_wait();  // what ran before has ended: memory may be read and written
     const uint32_t tm = tmem_base;
     volatile int *abort = &abort_flag;
     XIter<kCrossFwd> iter(a.sched, range);
@@ -127,6 +125,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (warp == kXTma) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
+            if (!a.sched.whole) a.pieces[blockIdx.x] = XIter<kCrossFwd>::first(a.sched, range);
             int nq = 0, ns = 0;  // items and stages loaded
             bool ok = true;
             while (ok && iter.next(it)) {
@@ -167,9 +166,8 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const int n_ks = a.d / 16;  // the head's own coordinates: the columns past d are zeros
             XRing stage, buf;
             int j = 0, n = 0;  // items, steps
-            // per score buffer (4 bits): the stage + 1 that its current step is the last to
-            // read, or 0.  A buffer found free releases that stage, which saves the
-            // accumulating warps a commit per block.
+            // per score buffer (4 bits): the stage + 1 that its current step, of a second tile,
+            // is the last to read, or 0.  A buffer found free releases that stage.
             uint32_t release = 0;
             bool ok = true;
             while (ok && iter.next(it)) {
@@ -185,8 +183,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         const uint64_t r = desc_at(r0, t * 16384);
                         uint64_t *sfull = &bars.sfull[x_half(it, t, j)][x];
                         const uint32_t done = (release >> (4 * x)) & 15u;
-                        release = (release & ~(15u << (4 * x))) |
-                                  ((t == it.n_tiles - 1 ? stage.i + 1u : 0u) << (4 * x));
+                        release = (release & ~(15u << (4 * x))) | ((t == 1 ? stage.i + 1u : 0u) << (4 * x));
                         ok = mbar_wait(&bars.bfree[x], buf.phase ^ 1, abort);  // the first round passes at once
                         if (!ok) break;
                         tc_fence_after();
@@ -241,6 +238,9 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             for (int ks = 0; ks < kBlk / 16; ++ks)
                                 mma_ts(acc, col + 8 * ks, desc_at(c, 2048 * ks), id, b > 0 || ks > 0);
                             mma_commit(&bars.bfree[buf.i]);
+                            // an item of one tile, whose steps wait for loads: its stage is free at
+                            // once (with two tiles the scores' warp knows when both are done)
+                            if (it.n_tiles == 1) mma_commit(&bars.empty[stage.i]);
                             if (b == it.n_blk - 1) mma_commit(&bars.ofull[me]);
                         }
                         buf.next(kBufs);

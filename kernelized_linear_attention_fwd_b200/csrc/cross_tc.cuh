@@ -117,6 +117,7 @@ inline cudaError_t x_launch(CrossMode mode, const CrossPlan &p, const CrossIo &i
     a = XArgs{};
     a.sched = p.sched[mode];
     a.sched.key_lengths = io.key_lengths;
+    a.sched.whole = cross_whole(p.sched[mode], io);
     a.d = p.d;
     a.stat_stride = p.R_pad;
     a.BH = p.BH;

@@ -99,14 +99,12 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constan
         }
         __syncwarp();
         const XRange r = x_range<MODE>(a.sched, blockIdx.x, gridDim.x, lane);
-        if (lane == 0) {
-            range = r;
-            if (!a.sched.whole) a.pieces[blockIdx.x] = XIter<MODE>::first(a.sched, r);
-        }
+        if (lane == 0) range = r;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    griddep_wait();  // what ran before has ended: memory may be read and written
     const uint32_t tm = tmem_base;
     volatile int *abort = &abort_flag;
     XIter<MODE> iter(a.sched, range);
@@ -115,6 +113,7 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constan
     if (warp == kBTma) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
+            if (!a.sched.whole) a.pieces[blockIdx.x] = XIter<MODE>::first(a.sched, range);
             int nq = 0, ns = 0;  // items and stages loaded
             XRing stage;
             bool ok = true;
@@ -397,9 +396,8 @@ cudaError_t launch_mode(const CrossPlan &p, const CrossIo &io, cudaStream_t st) 
     if (e != cudaSuccess) return e;
     if ((e = smem_opt_in_once<cross_bwd_kernel<MODE>>(kBSmem)) != cudaSuccess) return e;
     ProfScope prof(MODE == kCrossDq ? "cross_dq" : "cross_dkv", st);
-    cross_bwd_kernel<MODE>
-        <<<x.a.sched.grid, BCfg<MODE>::kThreads, kBSmem, st>>>(x.maps[0], x.maps[1], x.maps[2], x.maps[3], x.a);
-    return cudaGetLastError();
+    return launch_dependent(cross_bwd_kernel<MODE>, dim3(x.a.sched.grid), (unsigned)BCfg<MODE>::kThreads, kBSmem, st,
+                            x.maps[0], x.maps[1], x.maps[2], x.maps[3], x.a);
 }
 
 }  // namespace

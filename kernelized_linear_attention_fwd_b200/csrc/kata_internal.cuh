@@ -240,7 +240,7 @@ struct XSched {
     const int *key_lengths;
     int grid;
     int min_share;  // fewest units a CTA takes
-    int whole;      // cut at item boundaries only
+    int whole;      // cut at item boundaries only: 2: always, 1: if the lengths are equal
     int slot_rows;  // rows of a cut piece's partial sums
 };
 struct CrossPlan {
@@ -249,8 +249,9 @@ struct CrossPlan {
     long long BH;
     int R;             // rows per problem
     int R_pad;         // R rounded up to 128: row stride of the statistics
+    bool few;          // forward by launch_cross_few
     int splits[3];     // fp32, per CrossMode: pieces of the summed axis (1: no join)
-    XSched sched[3];   // bf16, per CrossMode
+    XSched sched[3];   // bf16, per CrossMode, and few
     // workspace (bytes)
     size_t ws_part[3];  // partial sums of each mode
     size_t ws_part_l;   // forward: partial denominators
@@ -267,9 +268,15 @@ struct CrossIo {
     void *dq, *dk, *dv;
     void *ws;
 };
+inline int cross_whole(const XSched &s, const CrossIo &io) { return s.whole == 2 || (s.whole && !io.key_lengths); }
 cudaError_t launch_cross_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 cudaError_t launch_cross_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
-// One mode's main kernel: bf16 on the tensor cores, fp32 on the CUDA cores.
+// One mode's main kernel: forward of at most kFewRows rows per key head; others in
+// bf16 on the tensor cores, in fp32 on the CUDA cores.
+constexpr int kFewRows = 4;
+// CTAs per SM of that kernel for this many rows (64, 80, 128 registers a thread).
+__host__ __device__ constexpr int few_per_sm(int rows) { return rows == 1 ? 4 : rows == 2 ? 3 : 2; }
+cudaError_t launch_cross_few(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 cudaError_t launch_cross_fwd_tc(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 cudaError_t launch_cross_bwd_tc(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 cudaError_t launch_cross_simt(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);

@@ -156,10 +156,12 @@ int cross_splits(long long items, long long steps, int min_steps) {
 }
 
 // The tensor cores' schedule of one mode.  Items are cut unless that gains little:
-// when whole items, dealt evenly, leave the busiest SM at most 3% more than the
-// average (many items, or a multiple of the grid), the join is not worth its launch.
-// A CTA takes at least 4 units (forward: 512 keys of a tile) of a cut item: below
-// that its start and the join cost more than the steps it saves.
+// - whole = 2: items at most 4 units long (below that a CTA's start and the join cost
+//   more than the steps saved), or 16 and more of them per SM;
+// - whole = 1: equal lengths and whole items, dealt evenly, that leave the busiest SM at
+//   most 3% above the average.  (Lengths that differ put stretches of whole items up
+//   to an item apart: 64 sequences of 1501 keys and less, 16 heads, one query: 64 us
+//   against %RAG% us cut.)
 bool cross_sched(const CrossPlan &p, CrossMode m, int rows, int cols, XSched &s) {
     const long long tiles = (rows + 127) / 128, tpi = cross_tc_tiles(m);
     const long long blocks = (cols + kXCols - 1) / kXCols;
@@ -172,12 +174,14 @@ bool cross_sched(const CrossPlan &p, CrossMode m, int rows, int cols, XSched &s)
     s.cols = cols;
     s.Tk = p.Tk;
     s.key_lengths = nullptr;
-    s.min_share = 4;
-    const long long rounds = (items + kPlanSms - 1) / kPlanSms;
-    s.whole = rounds * kPlanSms * 100 <= items * 103 || (items < kPlanSms && blocks * tpi <= s.min_share);
-    const long long most = s.whole ? items : (units + s.min_share - 1) / s.min_share;
-    s.grid = (int)(most < kPlanSms ? most : kPlanSms);
-    if (s.whole) s.min_share = 1;
+    // CTAs that run at a time, and the fewest units worth one
+    const int full = m == kCrossFwd && p.few ? few_per_sm(p.R) * kPlanSms : kPlanSms, least = m == kCrossFwd && p.few ? 2 : 4;
+    const long long rounds = (items + full - 1) / full;
+    const bool tiny = items < full && blocks * tpi <= least;
+    s.whole = tiny || items >= 16 * full ? 2 : rounds * full * 100 <= items * 103 ? 1 : 0;
+    s.min_share = s.whole == 2 ? 1 : least;
+    const long long most = s.whole == 2 ? items : (units + least - 1) / least;
+    s.grid = (int)(most < full ? most : full);
     const int most_rows = m == kCrossDq ? 128 : 256;  // forward: two tiles; dkv: dv's 128 rows and dk's
     s.slot_rows = m != kCrossDkv && rows < most_rows ? rows : most_rows;
     return true;
@@ -204,12 +208,14 @@ kata_status cross_plan(int B, int H, int Hkv, int Tq, int Tk, int d, kata_dtype 
     p.ws_delta = 0;
     p.ws_rden = stat;
     size_t off = 2 * stat;
+    p.few = p.R <= kFewRows;
     for (const CrossMode m : {kCrossFwd, kCrossDq, kCrossDkv}) {
         const long long n = m == kCrossDkv ? Tk : p.R, c = m == kCrossDkv ? p.R : Tk;
         size_t part_rows = 0;  // rows of partial sums
-        if (dtype == KATA_BF16) {
+        const bool cut = dtype == KATA_BF16 || (m == kCrossFwd && p.few);
+        if (cut) {
             if (!cross_sched(p, m, (int)n, (int)c, p.sched[m])) return KATA_ERR_UNSUPPORTED;
-            part_rows = p.sched[m].whole ? 0 : (size_t)p.sched[m].grid * 2 * p.sched[m].slot_rows;
+            part_rows = p.sched[m].whole == 2 ? 0 : (size_t)p.sched[m].grid * 2 * p.sched[m].slot_rows;
             p.splits[m] = 1;
         } else {
             const int t = cross_simt_rows(m, p);
@@ -219,7 +225,7 @@ kata_status cross_plan(int B, int H, int Hkv, int Tq, int Tk, int d, kata_dtype 
             if (p.splits[m] > 1) part_rows = (size_t)p.splits[m] * p.BH * n * (m == kCrossDkv ? 2 : 1);
         }
         const size_t part = align_up(part_rows * d * 4);
-        const size_t pieces = dtype == KATA_BF16 && part ? align_up(p.sched[m].grid * sizeof(XPiece)) : 0;
+        const size_t pieces = cut && part ? align_up(p.sched[m].grid * sizeof(XPiece)) : 0;
         if (m == kCrossFwd) {
             p.ws_part[m] = 0;
             p.ws_part_l = part;
