@@ -9,6 +9,7 @@ libkata.so is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -657,12 +658,12 @@ def _run(name, device, stream, *args):
     """Calls the C function `name`(*args, stream) with `device` current."""
     import torch
 
-    fn = getattr(load_library(), name)
+    fn = getattr(_lib or load_library(), name)
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(device.index)
     else:
         handle = _stream_handle(stream, device)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         st = fn(*args, handle)
     else:
         with _on_device(device):
@@ -683,21 +684,38 @@ def _new(stream, like, shape, dtype=None):
         return like.new_empty(shape, dtype=dtype)
 
 
+def _like(stream, t):
+    """Contiguous tensor of the shape and type of `t`, as _new."""
+    import torch
+
+    if stream is None or stream.device != t.device:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(query, *sizes):
+    """What the size query `query` returns: a function of its arguments only."""
+    return int(getattr(load_library(), query)(*sizes))
+
+
 def _token_major(t, name, heads=None, like=None):
     """t is a CUDA [B, T, H, d] tensor with a contiguous last axis (any other
     strides), matching `like` in B, T, d, dtype and device when given."""
     if not t.is_cuda:
         raise KataError(KATA_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
-    if t.dim() != 4:
-        raise KataError(KATA_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, want [B, T, H, d]")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    shape = t.shape
+    if len(shape) != 4:
+        raise KataError(KATA_ERR_INVALID_ARG, f"{name} has shape {tuple(shape)}, want [B, T, H, d]")
+    if shape[3] > 1 and t.stride(3) != 1:
         raise KataError(KATA_ERR_INVALID_ARG, f"the last axis of {name} must be contiguous")
     if like is not None:
         B, T, H, d = like.shape
-        want = (B, T, t.shape[2] if heads is None else heads, d)
-        if tuple(t.shape) != want:
-            raise KataError(KATA_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, want {want}")
-        if t.dtype != like.dtype:
+        want = (B, T, shape[2] if heads is None else heads, d)
+        if shape != want:
+            raise KataError(KATA_ERR_INVALID_ARG, f"{name} has shape {tuple(shape)}, want {want}")
+        if t.dtype is not like.dtype:
             raise KataError(KATA_ERR_INVALID_ARG, f"{name} has dtype {t.dtype}, want {like.dtype}")
         if t.device != like.device:
             raise KataError(KATA_ERR_INVALID_ARG, f"{name} is on {t.device}, want {like.device}")
@@ -775,7 +793,7 @@ def kata_qk_norm_rotate(q, k=None, q_weight=None, k_weight=None, inv_freq=None, 
 
 
 def kata_qk_norm_rotate_backward_workspace_bytes(B, T, Hq, Hk, d) -> int:
-    return int(load_library().kata_qk_norm_rotate_backward_workspace_bytes(B, T, Hq, Hk, d))
+    return _workspace_bytes("kata_qk_norm_rotate_backward_workspace_bytes", B, T, Hq, Hk, d)
 
 
 def kata_qk_norm_rotate_backward(dq_out, dk_out, q, k=None, q_weight=None, k_weight=None,
@@ -802,22 +820,22 @@ def kata_qk_norm_rotate_backward(dq_out, dk_out, q, k=None, q_weight=None, k_wei
             raise KataError(KATA_ERR_INVALID_ARG, "k without dk_out")
         _is(dk_out, "dk_out", (B, Hk, T, d), q.dtype, dev)
         if dk is None:
-            dk = _new(stream, q, (B, T, Hk, d))
+            dk = _like(stream, k)
         else:
             _token_major(dk, "dk", heads=Hk, like=q)
         if dk_weight is None:
-            dk_weight = _new(stream, q, (d,), torch.float32)
+            dk_weight = _new(stream, q, (d,), torch.float32) if k_weight is None else _like(stream, k_weight)
         else:
             _is(dk_weight, "dk_weight", (d,), torch.float32, dev)
     if dq is None:
-        dq = _new(stream, q, (B, T, Hq, d))
+        dq = _like(stream, q)
     else:
         _token_major(dq, "dq", heads=Hq, like=q)
     if dq_weight is None:
-        dq_weight = _new(stream, q, (d,), torch.float32)
+        dq_weight = _new(stream, q, (d,), torch.float32) if q_weight is None else _like(stream, q_weight)
     else:
         _is(dq_weight, "dq_weight", (d,), torch.float32, dev)
-    need = load_library().kata_qk_norm_rotate_backward_workspace_bytes(B, T, Hq, Hk, d)
+    need = _workspace_bytes("kata_qk_norm_rotate_backward_workspace_bytes", B, T, Hq, Hk, d)
     workspace, nbytes = _sized_workspace(workspace, need, q, stream)
     _run("kata_qk_norm_rotate_backward", dev, stream, dq_out.data_ptr(), _address(dk_out), q.data_ptr(),
          _address(k), _address(q_weight), _address(k_weight), _address(inv_freq) if n_rot else None,
@@ -861,7 +879,7 @@ def _cross_inputs(q, k, v, key_lengths):
 
 
 def kata_cross_forward_workspace_bytes(B, H, Hkv, Tq, Tk, d, dtype_code) -> int:
-    return int(load_library().kata_cross_forward_workspace_bytes(B, H, Hkv, Tq, Tk, d, dtype_code))
+    return _workspace_bytes("kata_cross_forward_workspace_bytes", B, H, Hkv, Tq, Tk, d, dtype_code)
 
 
 def kata_cross_forward(q, k, v, key_lengths=None, out=None, y_out=None, den_out=None,
@@ -877,14 +895,14 @@ def kata_cross_forward(q, k, v, key_lengths=None, out=None, y_out=None, den_out=
     dev = q.device
     code = _dtype_code(q)
     if out is None:
-        out = _new(stream, q, (B, H, Tq, d))
+        out = _like(stream, q)
     else:
         _is(out, "out", (B, H, Tq, d), q.dtype, dev)
     if y_out is not None:
         _is(y_out, "y_out", (B, H, Tq, d), torch.float32, dev)
     if den_out is not None:
         _is(den_out, "den_out", (B, H, Tq), torch.float32, dev)
-    need = load_library().kata_cross_forward_workspace_bytes(*sizes, code)
+    need = _workspace_bytes("kata_cross_forward_workspace_bytes", *sizes, code)
     workspace, nbytes = _sized_workspace(workspace, need, q, stream)
     _run("kata_cross_forward", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(key_lengths),
          out.data_ptr(), *sizes, code, _address(y_out), _address(den_out), _address(workspace), nbytes)
@@ -892,7 +910,7 @@ def kata_cross_forward(q, k, v, key_lengths=None, out=None, y_out=None, den_out=
 
 
 def kata_cross_backward_workspace_bytes(B, H, Hkv, Tq, Tk, d, dtype_code) -> int:
-    return int(load_library().kata_cross_backward_workspace_bytes(B, H, Hkv, Tq, Tk, d, dtype_code))
+    return _workspace_bytes("kata_cross_backward_workspace_bytes", B, H, Hkv, Tq, Tk, d, dtype_code)
 
 
 def kata_cross_backward(dout, q, k, v, y, den, key_lengths=None, dq=None, dk=None, dv=None,
@@ -907,15 +925,19 @@ def kata_cross_backward(dout, q, k, v, y, den, key_lengths=None, dq=None, dk=Non
     _is(dout, "dout", (B, H, Tq, d), q.dtype, dev)
     _is(y, "y", (B, H, Tq, d), torch.float32, dev)
     _is(den, "den", (B, H, Tq), torch.float32, dev)
-    grads = []
-    for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
-        if t is None:
-            t = _new(stream, q, like.shape)
-        else:
-            _is(t, name, like.shape, q.dtype, dev)
-        grads.append(t)
-    dq, dk, dv = grads
-    need = load_library().kata_cross_backward_workspace_bytes(*sizes, code)
+    if dq is None:
+        dq = _like(stream, q)
+    else:
+        _is(dq, "dq", (B, H, Tq, d), q.dtype, dev)
+    if dk is None:
+        dk = _like(stream, k)
+    else:
+        _is(dk, "dk", (B, Hkv, Tk, d), q.dtype, dev)
+    if dv is None:
+        dv = _like(stream, v)
+    else:
+        _is(dv, "dv", (B, Hkv, Tk, d), q.dtype, dev)
+    need = _workspace_bytes("kata_cross_backward_workspace_bytes", *sizes, code)
     workspace, nbytes = _sized_workspace(workspace, need, q, stream)
     _run("kata_cross_backward", dev, stream, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
          y.data_ptr(), den.data_ptr(), _address(key_lengths), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),

@@ -26,83 +26,106 @@
 #include <cuda_bf16.h>
 
 #include "kata_internal.cuh"
+#include "sm100.cuh"
 
 namespace kata {
 namespace {
 
+using namespace kata::sm100;
+
 constexpr int kNormWarps = 8;
 
-template <typename T>
-struct Vec4;
-template <>
-struct Vec4<float> {
-    using V = float4;
-};
-template <>
-struct Vec4<__nv_bfloat16> {
-    using V = uint2;
+// A lane's 4 pairs (a_j, b_j) of a row as packed fp32: a = (a_0 a_1), (a_2 a_3), b
+// likewise, whichever way the pairs lie in memory; all arithmetic is on these.
+struct Pairs {
+    uint64_t a[2], b[2];
 };
 
-__device__ __forceinline__ void unpack4(const float4 &v, float *x) {
-    x[0] = v.x;
-    x[1] = v.y;
-    x[2] = v.z;
-    x[3] = v.w;
-}
-__device__ __forceinline__ void unpack4(const uint2 &v, float *x) {
-    x[0] = __uint_as_float(v.x << 16);
-    x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(v.y << 16);
-    x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-}
-__device__ __forceinline__ void pack4(const float *x, float4 &v) { v = make_float4(x[0], x[1], x[2], x[3]); }
-__device__ __forceinline__ void pack4(const float *x, uint2 &v) {
-    __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-    v.x = *reinterpret_cast<uint32_t *>(&a);
-    v.y = *reinterpret_cast<uint32_t *>(&b);
-}
+__device__ __forceinline__ uint32_t lo16(uint32_t w) { return w << 16; }
+__device__ __forceinline__ uint32_t hi16(uint32_t w) { return w & 0xFFFF0000u; }
+__device__ __forceinline__ uint64_t both(float x) { return f32x2_pack(__float_as_uint(x), __float_as_uint(x)); }
 
-// The 8 elements of a lane as two vectors of 4 (half-split pairs: a_0..a_3 and
-// b_0..b_3; neighbouring pairs: a_0 b_0 a_1 b_1 and a_2 b_2 a_3 b_3).
-template <typename T>
-struct Row8 {
-    typename Vec4<T>::V v[2];
-    __device__ __forceinline__ void load(const T *row, int o0, int o1) {
-        v[0] = __ldg(reinterpret_cast<const typename Vec4<T>::V *>(row + o0));
-        v[1] = __ldg(reinterpret_cast<const typename Vec4<T>::V *>(row + o1));
-    }
-    __device__ __forceinline__ void store(T *row, int o0, int o1) const {
-        *reinterpret_cast<typename Vec4<T>::V *>(row + o0) = v[0];
-        *reinterpret_cast<typename Vec4<T>::V *>(row + o1) = v[1];
-    }
-    __device__ __forceinline__ void get(float *x) const {
-        unpack4(v[0], x);
-        unpack4(v[1], x + 4);
-    }
-    __device__ __forceinline__ void set(const float *x) {
-        pack4(x, v[0]);
-        pack4(x + 4, v[1]);
-    }
-};
-
-// Positions in x[8] of the pair j's members.
+// The 8 elements of a lane in memory: two vectors of 4 at offsets o0 and o1
+// (half-split pairs: a_0 .. a_3 and b_0 .. b_3; neighbouring pairs: a_0 b_0 a_1 b_1
+// and a_2 b_2 a_3 b_3).
+template <typename T, bool INTER>
+struct Row8;
 template <bool INTER>
-__device__ __forceinline__ constexpr int pa(int j) {
-    return INTER ? 2 * j : j;
-}
+struct Row8<__nv_bfloat16, INTER> {
+    uint2 v[2];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *row, int o0, int o1) {
+        v[0] = __ldg(reinterpret_cast<const uint2 *>(row + o0));
+        v[1] = __ldg(reinterpret_cast<const uint2 *>(row + o1));
+    }
+    __device__ __forceinline__ void zero() { v[0] = v[1] = make_uint2(0u, 0u); }
+    __device__ __forceinline__ Pairs get() const {
+        Pairs p;
+        if (INTER) {
+            p.a[0] = f32x2_pack(lo16(v[0].x), lo16(v[0].y));
+            p.b[0] = f32x2_pack(hi16(v[0].x), hi16(v[0].y));
+            p.a[1] = f32x2_pack(lo16(v[1].x), lo16(v[1].y));
+            p.b[1] = f32x2_pack(hi16(v[1].x), hi16(v[1].y));
+        } else {
+            p.a[0] = f32x2_pack(lo16(v[0].x), hi16(v[0].x));
+            p.a[1] = f32x2_pack(lo16(v[0].y), hi16(v[0].y));
+            p.b[0] = f32x2_pack(lo16(v[1].x), hi16(v[1].x));
+            p.b[1] = f32x2_pack(lo16(v[1].y), hi16(v[1].y));
+        }
+        return p;
+    }
+    __device__ __forceinline__ static void store(__nv_bfloat16 *row, int o0, int o1, const Pairs &p) {
+        uint2 w[2];
+        if (INTER) {
+            w[0] = make_uint2(pack_bf16x2(f32x2_lo(p.a[0]), f32x2_lo(p.b[0])),
+                              pack_bf16x2(f32x2_hi(p.a[0]), f32x2_hi(p.b[0])));
+            w[1] = make_uint2(pack_bf16x2(f32x2_lo(p.a[1]), f32x2_lo(p.b[1])),
+                              pack_bf16x2(f32x2_hi(p.a[1]), f32x2_hi(p.b[1])));
+        } else {
+            w[0] = make_uint2(f32x2_to_bf16x2(p.a[0]), f32x2_to_bf16x2(p.a[1]));
+            w[1] = make_uint2(f32x2_to_bf16x2(p.b[0]), f32x2_to_bf16x2(p.b[1]));
+        }
+        *reinterpret_cast<uint2 *>(row + o0) = w[0];
+        *reinterpret_cast<uint2 *>(row + o1) = w[1];
+    }
+};
 template <bool INTER>
-__device__ __forceinline__ constexpr int pb(int j) {
-    return INTER ? 2 * j + 1 : j + 4;
-}
+struct Row8<float, INTER> {
+    uint4 v[2];
+    __device__ __forceinline__ void load(const float *row, int o0, int o1) {
+        v[0] = __ldg(reinterpret_cast<const uint4 *>(row + o0));
+        v[1] = __ldg(reinterpret_cast<const uint4 *>(row + o1));
+    }
+    __device__ __forceinline__ void zero() { v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ Pairs get() const {
+        Pairs p;
+        if (INTER) {
+            p.a[0] = f32x2_pack(v[0].x, v[0].z);
+            p.b[0] = f32x2_pack(v[0].y, v[0].w);
+            p.a[1] = f32x2_pack(v[1].x, v[1].z);
+            p.b[1] = f32x2_pack(v[1].y, v[1].w);
+        } else {
+            p.a[0] = f32x2_pack(v[0].x, v[0].y);
+            p.a[1] = f32x2_pack(v[0].z, v[0].w);
+            p.b[0] = f32x2_pack(v[1].x, v[1].y);
+            p.b[1] = f32x2_pack(v[1].z, v[1].w);
+        }
+        return p;
+    }
+    __device__ __forceinline__ static void store(float *row, int o0, int o1, const Pairs &p) {
+        const float a0 = f32x2_lo(p.a[0]), a1 = f32x2_hi(p.a[0]), a2 = f32x2_lo(p.a[1]), a3 = f32x2_hi(p.a[1]);
+        const float b0 = f32x2_lo(p.b[0]), b1 = f32x2_hi(p.b[0]), b2 = f32x2_lo(p.b[1]), b3 = f32x2_hi(p.b[1]);
+        *reinterpret_cast<float4 *>(row + o0) = INTER ? make_float4(a0, b0, a1, b1) : make_float4(a0, a1, a2, a3);
+        *reinterpret_cast<float4 *>(row + o1) = INTER ? make_float4(a2, b2, a3, b3) : make_float4(b0, b1, b2, b3);
+    }
+};
 
-// The lane's offsets in a row and its four angles.
+// A lane's offsets in a row.
 template <int D, bool INTER>
 struct Lane {
-    int o0, o1;
-    float c[4], s[4];
+    int p0, o0, o1;  // first pair; the two runs of 4 elements
 
     __device__ __forceinline__ explicit Lane(int lane, int n_rot) {
-        const int p0 = 4 * (lane % (D / 8));
+        p0 = 4 * (lane % (D / 8));
         if (INTER) {
             o0 = 2 * p0;
             o1 = o0 + 4;
@@ -114,30 +137,28 @@ struct Lane {
             o1 = p0 + D / 2;
         }
     }
-
-    // Angle of pair `lane` for this token, shared through `buf` (one per warp).
-    // position * inv_freq is taken in 64 bits, reduced to a fraction of a turn
-    // there (at position 2^31 that still leaves 2^-22 of a turn), and only the
-    // fraction's sine and cosine are 32-bit.
-    __device__ __forceinline__ void angles(float2 *buf, int lane, long long pos, double turn_freq, int n_rot) {
-        __syncwarp();
-        if (lane < n_rot) {
-            const double turns = (double)pos * turn_freq;
-            float2 cs;
-            sincospif((float)(2.0 * (turns - rint(turns))), &cs.y, &cs.x);
-            buf[lane] = cs;
-        }
-        __syncwarp();
-        const int p0 = 4 * (lane % (D / 8));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool on = p0 + j < n_rot;
-            const float2 cs = on ? buf[p0 + j] : make_float2(1.f, 0.f);
-            c[j] = cs.x;
-            s[j] = cs.y;
-        }
+    // element e of the row's run order (a_0 .. a_3, b_0 .. b_3) in memory
+    __device__ __forceinline__ int at(int e) const {
+        const int j = e & 3;
+        if (INTER) return 2 * (p0 + j) + e / 4;
+        return (e < 4 ? o0 : o1) + j;
     }
 };
+
+// Cosine and sine of the angles of one token's pairs, shared by the warp through
+// `buf`: pair `lane` is worked out here.  position * inv_freq is taken in 64 bits,
+// reduced to a fraction of a turn there (at position 2^31 that still leaves 2^-22
+// of a turn), and only the fraction's sine and cosine are 32-bit.
+__device__ __forceinline__ void share_angles(float2 *buf, int lane, long long pos, double turn_freq, int n_rot) {
+    __syncwarp();
+    float2 cs = make_float2(1.f, 0.f);  // pairs that do not turn
+    if (lane < n_rot) {
+        const double turns = (double)pos * turn_freq;
+        sincospif((float)(2.0 * (turns - rint(turns))), &cs.y, &cs.x);
+    }
+    buf[lane] = cs;
+    __syncwarp();
+}
 
 // Sum over the lanes of one row.
 template <int D>
@@ -146,6 +167,18 @@ __device__ __forceinline__ float row_sum(float x) {
     for (int o = D / 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
+
+// Dot product of a lane's 8 elements.
+__device__ __forceinline__ float dot8(const Pairs &x, const Pairs &y) {
+    const uint64_t t = f32x2_fma(
+        x.b[1], y.b[1], f32x2_fma(x.b[0], y.b[0], f32x2_fma(x.a[1], y.a[1], f32x2_mul(x.a[0], y.a[0]))));
+    return f32x2_lo(t) + f32x2_hi(t);
+}
+
+// Row groups that a warp loads at a time: 2 KB, of the input or of input and gradient.
+__host__ __device__ constexpr int norm_groups(bool backward, int size) { return (backward ? 4 : 8) / size; }
+// Blocks per SM (64 and 80 registers a thread).
+__host__ __device__ constexpr int norm_per_sm(bool backward) { return backward ? 2 : 3; }
 
 template <typename T>
 struct NormArgs {
@@ -167,100 +200,146 @@ struct NormArgs {
     float eps;
 };
 
-// U row groups in flight per warp: at U = 4 a lane has 4 (forward) loads of 16
-// bytes outstanding, about 128 KB per SM at 64 warps.
+// A warp loads up to U row groups at a time; what is left of a token's heads goes
+// group by group.  Bound by the loads once the arithmetic is packed (fp32 pairs,
+// gains folded into the angles once per token): %NORM%.
 template <typename T, int D, bool INTER, bool BWD>
-__global__ void __launch_bounds__(32 * kNormWarps, BWD ? 3 : 4)
+__global__ void __launch_bounds__(32 * kNormWarps, norm_per_sm(BWD))
 norm_rotate_kernel(const NormArgs<T> a) {
-    constexpr int kLanes = D / 8, kRows = 32 / kLanes, U = BWD ? 2 : 4;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, U = norm_groups(BWD, sizeof(T));
+    using Row = Row8<T, INTER>;
     __shared__ float2 cs_buf[kNormWarps][32];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, sub = lane / kLanes;
-    Lane<D, INTER> L(lane, a.n_rot);
-    const double turn_freq = lane < a.n_rot ? (double)a.inv_freq[lane] * 0.15915494309189533577 : 0.0;
     __shared__ float w_buf[2][D];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, sub = lane / kLanes;
+    const Lane<D, INTER> L(lane, a.n_rot);
+    const double turn_freq = lane < a.n_rot ? (double)a.inv_freq[lane] * 0.15915494309189533577 : 0.0;
     for (int x = threadIdx.x; x < 2 * D; x += 32 * kNormWarps) {
         const float *src = x < D ? a.w[0] : a.w[1];
         (&w_buf[0][0])[x] = src ? src[x % D] : 1.f;
     }
     __syncthreads();
-    float dw[2][8] = {};
+    Pairs dw[2] = {};
 
-    const long long n_warps = (long long)gridDim.x * kNormWarps;
-    for (long long tok = (long long)blockIdx.x * kNormWarps + warp; tok < a.tokens; tok += n_warps) {
-        const long long b = tok / a.T_, t = tok - b * a.T_;
-        if (a.n_rot > 0)
-            L.angles(cs_buf[warp], lane, a.pos ? a.pos[b * a.pos_stride + t] : t, turn_freq, a.n_rot);
-        else
-            L.angles(cs_buf[warp], lane, 0, 0.0, 0);
+    // this warp's tokens, every n_warps-th, as (b, t)
+    const int n_warps = gridDim.x * kNormWarps, tok0 = blockIdx.x * kNormWarps + warp;
+    const int step_b = n_warps / a.T_, step_t = n_warps - step_b * a.T_;
+    int b = tok0 / a.T_, t = tok0 - b * a.T_;
+    int left = tok0 < a.tokens ? (int)((a.tokens - tok0 + n_warps - 1) / n_warps) : 0;
+    auto position = [&](int bb, int tt) { return a.pos ? a.pos[bb * a.pos_stride + tt] : (long long)tt; };
+    long long pos = left > 0 ? position(b, t) : 0;
+    for (; left > 0; --left) {
+        share_angles(cs_buf[warp], lane, pos, turn_freq, a.n_rot);
+        // the next token's place and position, a token ahead
+        int nb = b + step_b, nt = t + step_t;
+        if (nt >= a.T_) {
+            nt -= a.T_;
+            ++nb;
+        }
+        if (left > 1) pos = position(nb, nt);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const int H = a.H[m];
-            float w[8];
-            *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(&w_buf[m][L.o0]);
-            *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(&w_buf[m][L.o1]);
-            const T *xt = a.x[m] + b * a.sb[m] + t * a.st[m];
-            const long long yt = (b * H * a.T_ + t) * D;  // head h adds h T D
-            for (int h0 = blockIdx.y * (U * kRows); h0 < H; h0 += gridDim.y * (U * kRows)) {
-                Row8<T> rx[U], rg[U];
+            if (H == 0) continue;
+            Pairs w, c, s;  // c in a: cosine; s in a: sine, in b: -sine
+            {
+                const float4 u = *reinterpret_cast<const float4 *>(&cs_buf[warp][L.p0]);
+                const float4 v = *reinterpret_cast<const float4 *>(&cs_buf[warp][L.p0 + 2]);
+                c.a[0] = f32x2_pack(__float_as_uint(u.x), __float_as_uint(u.z));
+                c.a[1] = f32x2_pack(__float_as_uint(v.x), __float_as_uint(v.z));
+                s.a[0] = f32x2_pack(__float_as_uint(u.y), __float_as_uint(u.w));
+                s.a[1] = f32x2_pack(__float_as_uint(v.y), __float_as_uint(v.w));
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int h = h0 + u * kRows + sub;
-                    if (h < H) {
-                        rx[u].load(xt + h * a.sh[m], L.o0, L.o1);
-                        if (BWD) rg[u].load(a.gy[m] + yt + (long long)h * a.T_ * D, L.o0, L.o1);
-                    } else {
-                        const float zero[8] = {};
-                        rx[u].set(zero);
-                        if (BWD) rg[u].set(zero);
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int h = h0 + u * kRows + sub;
-                    float x[8], o[8];
-                    rx[u].get(x);
-                    float ss = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-                    const float r = rsqrtf(fmaf(row_sum<D>(ss), 1.f / D, a.eps));
-                    if (!BWD) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] *= w[e];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float za = x[pa<INTER>(j)], zb = x[pb<INTER>(j)];
-                            o[pa<INTER>(j)] = r * fmaf(za, L.c[j], -zb * L.s[j]);
-                            o[pb<INTER>(j)] = r * fmaf(za, L.s[j], zb * L.c[j]);
-                        }
-                        rx[u].set(o);
-                        if (h < H) rx[u].store(a.y[m] + yt + (long long)h * a.T_ * D, L.o0, L.o1);
-                    } else {
-                        float g[8];
-                        rg[u].get(g);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {  // the gradient turned back
-                            const float ya = g[pa<INTER>(j)], yb = g[pb<INTER>(j)];
-                            g[pa<INTER>(j)] = fmaf(ya, L.c[j], yb * L.s[j]);
-                            g[pb<INTER>(j)] = fmaf(yb, L.c[j], -ya * L.s[j]);
-                        }
-                        float dot = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            x[e] *= r;  // u
-                            dw[m][e] = fmaf(g[e], x[e], dw[m][e]);
-                            g[e] *= w[e];
-                            dot = fmaf(g[e], x[e], dot);
-                        }
-                        const float mean = row_sum<D>(dot) * (1.f / D);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] = r * fmaf(-mean, x[e], g[e]);
-                        rx[u].set(o);
-                        if (h < H)
-                            rx[u].store(a.dx[m] + b * a.db[m] + t * a.dt[m] + h * a.dh[m], L.o0, L.o1);
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    s.b[i] = s.a[i] ^ 0x8000000080000000ull;
+                    w.a[i] = f32x2_pack(__float_as_uint(w_buf[m][L.at(2 * i)]),
+                                        __float_as_uint(w_buf[m][L.at(2 * i + 1)]));
+                    w.b[i] = f32x2_pack(__float_as_uint(w_buf[m][L.at(4 + 2 * i)]),
+                                        __float_as_uint(w_buf[m][L.at(5 + 2 * i)]));
                 }
             }
+            Pairs ca, cb;  // forward: y_a = x_a ca.a + x_b cb.a, y_b = x_a ca.b + x_b cb.b
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                ca.a[i] = f32x2_mul(c.a[i], w.a[i]);
+                cb.a[i] = f32x2_mul(s.b[i], w.b[i]);
+                ca.b[i] = f32x2_mul(s.a[i], w.a[i]);
+                cb.b[i] = f32x2_mul(c.a[i], w.b[i]);
+            }
+            const int h0 = blockIdx.y * (U * kRows) + sub, stride = gridDim.y * (U * kRows);
+            const long long sh = a.sh[m] * kRows, yh = (long long)a.T_ * D * kRows;
+            const T *px = a.x[m] + b * a.sb[m] + t * a.st[m] + h0 * a.sh[m];
+            const long long y0 = (((long long)b * H + h0) * a.T_ + t) * D;
+
+            auto work = [&](const Row &rx, const Row &rg, T *dst, bool on) {
+                Pairs x = rx.get(), o;
+                const float r = rsqrtf(fmaf(row_sum<D>(dot8(x, x)), 1.f / D, a.eps));
+                const uint64_t r2 = both(r);
+                if (!BWD) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        o.a[i] = f32x2_mul(f32x2_fma(x.a[i], ca.a[i], f32x2_mul(x.b[i], cb.a[i])), r2);
+                        o.b[i] = f32x2_mul(f32x2_fma(x.a[i], ca.b[i], f32x2_mul(x.b[i], cb.b[i])), r2);
+                    }
+                } else {
+                    const Pairs y = rg.get();
+                    Pairs g;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        // the gradient turned back
+                        g.a[i] = f32x2_fma(y.a[i], c.a[i], f32x2_mul(y.b[i], s.a[i]));
+                        g.b[i] = f32x2_fma(y.b[i], c.a[i], f32x2_mul(y.a[i], s.b[i]));
+                        x.a[i] = f32x2_mul(x.a[i], r2);  // u
+                        x.b[i] = f32x2_mul(x.b[i], r2);
+                        dw[m].a[i] = f32x2_fma(g.a[i], x.a[i], dw[m].a[i]);
+                        dw[m].b[i] = f32x2_fma(g.b[i], x.b[i], dw[m].b[i]);
+                        g.a[i] = f32x2_mul(g.a[i], w.a[i]);
+                        g.b[i] = f32x2_mul(g.b[i], w.b[i]);
+                    }
+                    const uint64_t nm2 = both(row_sum<D>(dot8(g, x)) * (-1.f / D));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        o.a[i] = f32x2_mul(f32x2_fma(nm2, x.a[i], g.a[i]), r2);
+                        o.b[i] = f32x2_mul(f32x2_fma(nm2, x.b[i], g.b[i]), r2);
+                    }
+                }
+                if (on) Row::store(dst, L.o0, L.o1, o);
+            };
+
+            T *po = BWD ? a.dx[m] + b * a.db[m] + t * a.dt[m] + h0 * a.dh[m] : a.y[m] + y0;
+            const long long oh = BWD ? a.dh[m] * kRows : yh;
+            const T *pg = BWD ? a.gy[m] + y0 : nullptr;
+            int h = h0;
+            for (; h - sub + U * kRows <= H; h += stride) {
+                Row rx[U], rg[BWD ? U : 1];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    rx[u].load(px + u * sh, L.o0, L.o1);
+                    if (BWD) rg[u].load(pg + u * yh, L.o0, L.o1);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) work(rx[u], rg[BWD ? u : 0], po + u * oh, true);
+                px += gridDim.y * (U * sh);
+                po += gridDim.y * (U * oh);
+                if (BWD) pg += gridDim.y * (U * yh);
+            }
+            // the set of groups that reaches past the last head, if it is this block's
+            for (int u = 0; u < U && h - sub < H; ++u, h += kRows) {
+                Row rx, rg;
+                const bool on = h < H;
+                rx.zero();
+                rg.zero();
+                if (on) {
+                    rx.load(px, L.o0, L.o1);
+                    if (BWD) rg.load(pg, L.o0, L.o1);
+                }
+                work(rx, rg, po, on);
+                px += sh;
+                po += oh;
+                if (BWD) pg += yh;
+            }
         }
+        b = nb;
+        t = nt;
     }
     if (BWD) {
         // the block's sum of dw: lanes of one column, then warps, always in this order
@@ -269,10 +348,11 @@ norm_rotate_kernel(const NormArgs<T> a) {
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float v = dw[m][e];
+                const uint64_t q = e < 4 ? dw[m].a[(e & 3) / 2] : dw[m].b[(e & 3) / 2];
+                float v = e & 1 ? f32x2_hi(q) : f32x2_lo(q);
 #pragma unroll
                 for (int o = kLanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (sub == 0) red[warp][m][(e < 4 ? L.o0 : L.o1) + (e & 3)] = v;
+                if (sub == 0) red[warp][m][L.at(e)] = v;
             }
         __syncthreads();
         if (threadIdx.x < 2 * D) {
@@ -309,7 +389,7 @@ norm_dw_kernel(const float *partial, int n, float *dwq, float *dwk) {
     }
 }
 
-// Blocks of the launch: as many as hold the tokens, at most 4 per SM (32 warps);
+// Blocks of the launch: as many as hold the tokens, at most what the SMs hold at a time;
 // if the tokens fill less than that, the heads are spread over grid.y.
 template <typename T, int D, bool INTER, bool BWD>
 cudaError_t launch_one(const NormRotate &p, cudaStream_t st) {
@@ -369,10 +449,10 @@ cudaError_t launch_t(const NormRotate &p, cudaStream_t st) {
 dim3 norm_rotate_grid(const NormRotate &p) {
     const long long tokens = (long long)p.B * p.T;
     const long long blocks = (tokens + kNormWarps - 1) / kNormWarps;
-    const long long full = 4LL * kPlanSms;
+    const long long full = (long long)norm_per_sm(p.backward) * kPlanSms;
     const int gx = (int)(blocks < full ? blocks : full);
     // row groups a warp could leave to others
-    const int rows = (p.backward ? 2 : 4) * (256 / p.d);
+    const int rows = norm_groups(p.backward, p.dtype == KATA_BF16 ? 2 : 4) * (256 / p.d);
     const int hm = p.H[0] > p.H[1] ? p.H[0] : p.H[1];
     const int groups = (hm + rows - 1) / rows;
     int gy = (int)(full / gx);
