@@ -132,7 +132,48 @@ def load_library(path: str = LIB_PATH):
     lib.kata_get_device_status.restype = i32
     lib.kata_get_device_status.argtypes = [vp]
     _lib = lib
+    _bind_calls(lib)
     return lib
+
+
+# The short cut of the short calls (csrc/torch_calls.cpp), or None: every call below
+# that takes it also works without it, through the same C functions.
+_calls = None
+
+
+def _bind_calls(lib):
+    global _calls
+    path = os.path.join(_HERE, "_calls.so")
+    if not os.path.exists(path):
+        return
+    import importlib.util
+
+    try:
+        import torch  # noqa: F401  (loads its libraries)
+
+        spec = importlib.util.spec_from_file_location("_calls", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    except ImportError:  # built against another torch or Python
+        return
+    mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.kata_qk_norm_rotate, lib.kata_qk_norm_rotate_backward,
+        lib.kata_qk_norm_rotate_backward_workspace_bytes, lib.kata_cross_forward,
+        lib.kata_cross_forward_workspace_bytes, lib.kata_cross_backward,
+        lib.kata_cross_backward_workspace_bytes)))
+    _calls = mod
+
+
+def _short(name, *args):
+    """The short cut's outputs, or NotImplemented where it does not take the call."""
+    if _lib is None:
+        load_library()
+    if _calls is None:
+        return NotImplemented
+    r = getattr(_calls, name)(*args)
+    if type(r) is int:
+        raise KataError(r, "kata_" + name)
+    return r
 
 
 def kata_version() -> int:
@@ -639,8 +680,10 @@ def kata_state_unpack(state_p, z_p, state=None, z=None, stream=None):
 
 
 # The calls below are short next to Python's share of them (a decode step's
-# kernels take 3 to 5 us), so their checks are one expression per tensor, with the
-# message worked out only on failure, and the device is switched only if needed.
+# kernels take 3 to 5 us), so they try the short cut first; what it does not take
+# (a given stream, another device than the current one, arguments to be refused)
+# goes through the checks here, one expression per tensor, with the message worked
+# out only on failure.
 _I64x3 = ctypes.c_int64 * 3
 
 
@@ -772,6 +815,11 @@ def kata_qk_norm_rotate(q, k=None, q_weight=None, k_weight=None, inv_freq=None, 
     by position * inv_freq [n_rot] fp32 (None: no rotation).  positions: int64
     [B,T] or [T] (None: 0 .. T-1).  interleaved: pairs (2i, 2i+1) instead of
     (i, i + n_rot)."""
+    if stream is None:
+        r = _short("qk_norm_rotate", q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved,
+                   q_out, k_out)
+        if r is not NotImplemented:
+            return r
     B, T, Hq, Hk, d, n_rot, pos_stride = _norm_inputs(q, k, q_weight, k_weight, inv_freq, positions)
     dev = q.device
     code = _dtype_code(q)
@@ -807,6 +855,11 @@ def kata_qk_norm_rotate_backward(dq_out, dk_out, q, k=None, q_weight=None, k_wei
     Without k, dk and dk_weight are None."""
     import torch
 
+    if stream is None:
+        r = _short("qk_norm_rotate_backward", q, k, q_weight, k_weight, inv_freq, positions, eps,
+                   interleaved, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace)
+        if r is not NotImplemented:
+            return r
     B, T, Hq, Hk, d, n_rot, pos_stride = _norm_inputs(q, k, q_weight, k_weight, inv_freq, positions)
     dev = q.device
     code = _dtype_code(q)
@@ -891,6 +944,10 @@ def kata_cross_forward(q, k, v, key_lengths=None, out=None, y_out=None, den_out=
     weights, which kata_cross_backward reads."""
     import torch
 
+    if stream is None:
+        r = _short("cross_forward", q, k, v, key_lengths, out, y_out, den_out, workspace)
+        if r is not NotImplemented:
+            return r
     B, H, Hkv, Tq, Tk, d = sizes = _cross_inputs(q, k, v, key_lengths)
     dev = q.device
     code = _dtype_code(q)
@@ -919,6 +976,10 @@ def kata_cross_backward(dout, q, k, v, y, den, key_lengths=None, dq=None, dk=Non
     and what it wrote to y_out and den_out for the same q, k, v, key_lengths."""
     import torch
 
+    if stream is None:
+        r = _short("cross_backward", q, k, v, key_lengths, dout, y, den, dq, dk, dv, workspace)
+        if r is not NotImplemented:
+            return r
     B, H, Hkv, Tq, Tk, d = sizes = _cross_inputs(q, k, v, key_lengths)
     dev = q.device
     code = _dtype_code(q)
