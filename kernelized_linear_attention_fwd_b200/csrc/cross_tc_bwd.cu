@@ -198,7 +198,7 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constan
         // ------------------------------------------------------------ products that accumulate
         if (lane == 0 && (kDkv || warp == kBAcc)) {
             const int me = warp - kBAcc;  // dkv: 0: dV from w / l and dY, 1: dK from ds and Q
-            const uint32_t id = idesc_bf16(128, 64, 0, 1);
+            const uint32_t id = idesc_bf16(128, a.d, 0, 1);  // the head's own columns
             const uint64_t dC = desc_sw128(smem_u32(sm_ring + (kDkv && me == 0 ? kBOp : 0)), 8192, 1024);
             XRing stage, buf, acc;  // acc: dq, the accumulator of the item
             uint32_t ophase = 1;    // dkv: the accumulator's first use passes at once

@@ -1,8 +1,7 @@
 // Short cut of the Python binding for the calls whose kernels take a few
 // microseconds: checks, output allocation and the C call in one step instead of
-// some forty Python operations (a decode step's head norm: 20 us of host time in
-// Python, %HN% here; both sides of the gradient of a small cross attention:
-// %HG%).
+// some forty Python operations (host time of a decode step's head norm: 20 us in
+// Python, 8 here; of the gradient of a small cross attention: 26 and 14).
 //
 // Every function takes the binding's arguments by position and either makes the
 // call and returns its outputs, or returns the library's status (an int) when the
