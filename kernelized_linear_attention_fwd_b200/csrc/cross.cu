@@ -244,7 +244,7 @@ cudaError_t launch_cut_join(const CrossPlan &p, const CrossIo &io, cudaStream_t 
 cudaError_t launch_main(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     if (mode == kCrossFwd && p.few) return launch_cross_few(p, io, st);
     if (p.dtype != KATA_BF16) return launch_cross_simt(mode, p, io, st);
-    return mode == kCrossFwd ? launch_cross_fwd_tc(p, io, st) : launch_cross_bwd_tc(mode, p, io, st);
+    return launch_cross_tc(mode, p, io, st);
 }
 
 template <typename T>

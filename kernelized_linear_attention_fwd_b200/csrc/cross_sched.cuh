@@ -1,14 +1,12 @@
 // How the tensor-core cross attention shares its work out (cross_tc.cu), and which
 // pieces of an item the join adds up (cross.cu).
 //
-// The work of one mode is a line of units (128-row tile, column block): sequence b
+// The work of one mode is a line of units (128-row tile, 128-column block): sequence b
 // has Hkv T_b N_b of them, T_b row tiles and N_b column blocks; in the forward and
-// dq passes N_b follows the sequence's visible keys, in dkv T_b does.  Items are
-// one tile of one head (backward) or two (forward); CTA c of G takes the units [c S, (c + 1) S),
-// S = max(ceil(total / G), min_share), cut at block boundaries (an item of two
-// tiles steps two units at a time; a cut inside one is moved down).  So every CTA
-// has the same work to within a block whatever the lengths are, and few long items
-// are split over all CTAs.  Plans whose items fill the grid many times over do not
+// dq passes N_b follows the sequence's visible keys, in dkv T_b does.  An item is
+// one tile of one head; CTA c of G takes the units [c S, (c + 1) S),
+// S = max(ceil(total / G), min_share).  So every CTA has the same work whatever the
+// lengths are, and few long items are split over all CTAs.  Plans whose items fill the grid many times over do not
 // cut (whole): there the cuts are moved down to item boundaries.
 #pragma once
 
@@ -17,9 +15,9 @@
 namespace kata {
 
 constexpr int kXCols = 128;  // columns of a block
-__host__ __device__ constexpr int cross_tc_tiles(int mode) { return mode == kCrossFwd ? 2 : 1; }
+constexpr int kXTile = 128;  // rows of a tile
 
-// A place in the line: block `blk` of item `p` of head `h` of sequence `b`.
+// A place in the line: block `blk` of tile `p` of head `h` of sequence `b`.
 struct XPos {
     int b, h, p, blk;
 };
@@ -34,7 +32,7 @@ struct alignas(16) XPiece {
 };
 // A stretch of blocks of one item.
 struct XItem {
-    int bh, r0, n_tiles, b0, n_blk;
+    int bh, r0, b0, n_blk;
     int cols;  // columns in use (dkv: all of them)
     int live;  // visible keys of the sequence
     int part;  // slot of a cut item's piece, or -1
@@ -46,23 +44,19 @@ template <int MODE>
 __device__ __forceinline__ void x_extent(const XSched &s, int b, int &live, int &tiles, int &blocks) {
     live = cross_length(s.key_lengths, b, s.Tk);
     const int rows = MODE == kCrossDkv ? live : s.rows, cols = MODE == kCrossDkv ? s.cols : live;
-    tiles = (rows + 127) / 128;
+    tiles = (rows + kXTile - 1) / kXTile;
     blocks = (cols + kXCols - 1) / kXCols;
 }
 
 // Place of unit `off` of sequence b.
-template <int MODE>
 __device__ __forceinline__ XPos x_place(const XSched &s, int b, long long off, int tiles, int blocks) {
-    constexpr int TPI = cross_tc_tiles(MODE);
     const long long per_head = (long long)tiles * blocks;
     XPos r;
     r.b = b;
     r.h = (int)(off / per_head);
     const long long rem = off - r.h * per_head;
-    r.p = (int)(rem / ((long long)TPI * blocks));
-    const int in_item = (int)(rem - r.p * ((long long)TPI * blocks));
-    const int nt = min(TPI, tiles - TPI * r.p);
-    r.blk = s.whole ? 0 : in_item / nt;
+    r.p = (int)(rem / blocks);
+    r.blk = s.whole ? 0 : (int)(rem - (long long)r.p * blocks);
     return r;
 }
 
@@ -119,14 +113,14 @@ struct XLine {
                 x_extent<MODE>(s, 0, live, tiles, blocks);
                 const long long per = (long long)s.Hkv * tiles * blocks;
                 const int b = (int)(u / per);
-                r = x_place<MODE>(s, b, u - b * per, tiles, blocks);
+                r = x_place(s, b, u - b * per, tiles, blocks);
             } else {
                 for (int b = first; b < last; ++b) {
                     int live, tiles, blocks;
                     x_extent<MODE>(s, b, live, tiles, blocks);
                     const long long per = (long long)s.Hkv * tiles * blocks;
                     if (u < at + per) {
-                        r = x_place<MODE>(s, b, u - at, tiles, blocks);
+                        r = x_place(s, b, u - at, tiles, blocks);
                         break;
                     }
                     at += per;
@@ -171,7 +165,6 @@ struct XIter {
     }
 
     __device__ __forceinline__ bool next(XItem &it) {
-        constexpr int TPI = cross_tc_tiles(MODE);
         while (at.b < s.B) {
             if (at.b == to.b && at.h == to.h && at.p == to.p && at.blk == to.blk) return false;
             int live, tiles, blocks;
@@ -183,8 +176,7 @@ struct XIter {
             const bool cut = at.b == to.b && at.h == to.h && at.p == to.p;
             const int end = cut ? to.blk : blocks;
             it.bh = at.b * s.Hkv + at.h;
-            it.r0 = at.p * TPI * 128;
-            it.n_tiles = min(TPI, tiles - TPI * at.p);
+            it.r0 = at.p * kXTile;
             it.b0 = at.blk;
             it.n_blk = end - at.blk;
             it.cols = MODE == kCrossDkv ? s.cols : live;
@@ -196,7 +188,7 @@ struct XIter {
                 at.blk = end;
             } else {
                 at.blk = 0;
-                if (++at.p * TPI >= tiles) {
+                if (++at.p == tiles) {
                     at.p = 0;
                     if (++at.h == s.Hkv) {
                         at.h = 0;
@@ -209,9 +201,6 @@ struct XIter {
         return false;
     }
 };
-
-// The half (warps 0-3 or 4-7) of the forward that takes tile t of the CTA's j-th item.
-__device__ __forceinline__ int x_half(const XItem &it, int t, int j) { return it.n_tiles == 2 ? t : j & 1; }
 
 // First row of a slot in the partial sums.
 __device__ __forceinline__ long long x_part_row(const XSched &s, int part) {

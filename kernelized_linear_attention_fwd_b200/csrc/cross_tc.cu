@@ -10,10 +10,10 @@
 // Every pass keeps 128-row tiles of its accumulators in tensor memory, walks the
 // other axis in blocks of 128 and forms per block
 //
-//   forward (here)   rows = queries  S = Q K^T             O  += bf16(w) V
-//   dq  (_bwd.cu)    rows = queries  S = Q K^T, P = dY V^T  dQ += bf16(s (p - D)) K
-//   dkv (_bwd.cu)    rows = keys     S = K Q^T, P = V dY^T  dV += bf16(w / l) dY
-//                                                           dK += bf16(ds / 2) Q
+//   forward  rows = queries  S = Q K^T              O  += bf16(w) V
+//   dq       rows = queries  S = Q K^T, P = dY V^T  dQ += bf16(s (p - D)) K
+//   dkv      rows = keys     S = K Q^T, P = V dY^T  dV += bf16(w / l) dY
+//                                                   dK += bf16(ds / 2) Q
 //
 // The weights are polynomial: no running maximum, no rescaling, so pieces of a
 // long axis add up, and the backward pass recomputes s exactly as the forward
@@ -22,44 +22,68 @@
 // depend on order.
 //
 // Roundings to bf16: the weights (and ds) that go back into the tensor cores as
-// operands, once each.  The denominator sums the rounded weights, so the rows
-// remain convex combinations of values: with one visible key y = v exactly and,
-// D being formed from the same y in fp32, the gradient of q and k is then zero up
-// to fp32 rounding instead of up to bf16 rounding.
+// operands, once each.  In the forward of a training step (EXACT) the denominator sums
+// the rounded weights, so that y is a convex combination of values to fp32: with one
+// visible key y = v and, D being formed from the same y, the gradient of q and k is
+// zero up to fp32 rounding instead of up to bf16 rounding.  Without y_out it sums them
+// unrounded, which leaves half of the arithmetic (8192 queries, 16384 keys, 8 heads:
+// 265 us against 295), and the output is within its own rounding of the same.
 //
 // Schedule.  The work is a line of units, one per (128-row tile, column block),
 // sequence by sequence; every CTA of the persistent grid takes an equal stretch
 // of it (cross_sched.cuh), whatever the lengths, and walks the stretch item by
 // item.  An item that a stretch boundary cuts is written as partial sums and
-// joined (cross.cu).  A forward item is two tiles, which share the keys and values
-// they read.  Warp 8 loads (TMA), warp 9 issues the products that form scores into
-// one of three score buffers of 128 columns, warps 0-3 and 4-7 turn the scores of
-// one tile each into weights, stored over the scores, and warps 10 and 11 issue the
-// products that accumulate.  Items of one tile go to the two halves in turn, each
-// with its own accumulator, so that one's epilogue overlaps the other's steps.
+// joined (cross.cu).
+//
+// A step is one tile against one block.  Tensor memory holds
+//
+//   0 .. 127       accumulators: forward, dq: two of 64 columns, items in turn;
+//                  dkv: dV and dK
+//   128, 256       S of successive steps (forward: and 384); the weights replace it:
+//                  per 16 scores 8 columns of w (SPLIT: and 8 of low parts), of ds, or
+//                  of w / l and 8 of ds
+//   384            dq, dkv: P, free again once the warps have read it
+//
+// so the next step's S is formed while this step's scores are turned, its P right
+// after them, and a step's accumulation overlaps the next one's scores.  128-column
+// score products run at the full rate (N = 64 ones pay for reading the 128-row
+// operand twice as often: a 64-column form of the backward passes took 1.6 times as
+// long).  One warp loads (TMA), one issues S, one P, one or two (dkv) accumulate.
+// 16 warps turn scores into weights, 32 columns each of their 32 rows (dkv with 8 warps
+// of 64 columns took 207 us where 16 take 189: 4 sequences of 16 heads, 2048 queries,
+// 4096 keys, ragged); dq, with half of dkv's arithmetic, has 8 (143 us; 16: 147).
 #include "cross_tc.cuh"
 
 namespace kata {
 namespace {
 
-constexpr int kXThreads = 384;
-constexpr int kXTma = 8, kXScore = 9, kXAcc = 10;  // and 11
-constexpr int kBlk = 128;                           // keys of a step
-constexpr int kSlot = 2 * 16384;                    // bytes of an item's queries
-constexpr int kOp = kBlk * 128;                     // bytes of a block's keys (or values)
-constexpr int kStage = 2 * kOp;
-constexpr int kStages = 5;
-constexpr int kSmem = 2 * kSlot + kStages * kStage + 1024;
-constexpr int kBufs = 3;
-constexpr uint32_t kBuf0 = 128;  // first score buffer's column; the halves' accumulators lie at 0 and 64
+template <int MODE>
+struct XCfg {
+    static constexpr bool kFwd = MODE == kCrossFwd, kDkv = MODE == kCrossDkv;
+    // groups of 4 warps that turn scores into weights, and the other warps behind them
+    static constexpr int kGroups = MODE == kCrossDq ? 2 : 4;
+    static constexpr int kTma = 4 * kGroups, kS = kTma + 1, kP = kFwd ? -1 : kTma + 2, kAcc = kTma + (kFwd ? 2 : 3);
+    static constexpr int kThreads = 32 * (kFwd ? kAcc + 1 : kAcc + 2);
+    static constexpr int kCols = kXCols / kGroups;  // columns of a step that a group turns
+    static constexpr int kRowOps = kFwd ? 1 : 2;
+    static constexpr int kSlot = kRowOps * 16384;  // an item's row operands
+    static constexpr int kOp = kXCols * 128;       // one column operand of a block
+    static constexpr int kStage = 2 * kOp;
+    static constexpr int kStages = kFwd ? 5 : 4;
+    static constexpr int kStat = kDkv ? 1024 : 0;  // -D and 1 / l of the block's queries
+    static constexpr int kSmem = 2 * kSlot + kStages * (kStage + kStat) + 1024;
+    // tensor memory: accumulators in columns 0 .. 127, regions of S, the one of P
+    static constexpr int kRegions = kFwd ? 3 : 2;
+    static constexpr uint32_t kColS = 128, kColP = 384;
+};
 
+template <int MODE>
 struct XBars {
-    uint64_t qfull[2], qempty[2], full[kStages], empty[kStages], bfree[kBufs], ofull[2], ofree[2], drain[3];
-    // scores formed and weights stored, per half and buffer: a half (and the warp
-    // that accumulates for it) waits for its own steps only, so with one barrier
-    // per buffer it could fall two phases behind the other half's steps and take
-    // a completed phase for its own.
-    uint64_t sfull[2][kBufs], pfull[2][kBufs];
+    using C = XCfg<MODE>;
+    uint64_t qfull[2], qempty[2], full[C::kStages], empty[C::kStages];
+    // per S region: scores formed, weights stored, products done; P formed, P read
+    uint64_t sfull[C::kRegions], wfull[C::kRegions], sfree[C::kRegions], pfull, pfree;
+    uint64_t ofull[2], ofree[2], drain[4];
 };
 
 // SPLIT: the weights as two bf16 numbers each (high and low part), which takes twice
@@ -68,57 +92,61 @@ struct XBars {
 // with one sign: next to the other roundings it is as 1 / sqrt(d).  Error of dq
 // relative to exact, rms, without and with (0.00166 of it the output's rounding):
 // d = 16 0.0026, 0.0025; d = 32 0.0025, 0.0024; d = 64 0.0024, 0.0024.  For d = 64 it
-// would take the forward of 2048 queries on 4096 keys from 125 to 202 us.
-template <bool SPLIT>
-__global__ void __launch_bounds__(kXThreads, 1)
-cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const XArgs a) {
+// would take the forward of 2048 queries on 4096 keys half as long again.
+template <int MODE, bool SPLIT, bool EXACT>
+__global__ void __launch_bounds__(XCfg<MODE>::kThreads, 1)
+cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant__ CUtensorMap tm_r1,
+                 const __grid_constant__ CUtensorMap tm_c0, const __grid_constant__ CUtensorMap tm_c1,
+                 const XArgs a) {
+    using C = XCfg<MODE>;
+    constexpr bool kFwd = C::kFwd, kDkv = C::kDkv;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ XBars bars;
+    __shared__ XBars<MODE> bars;
     __shared__ XRange range;
+    __shared__ float lsum[kFwd ? 2 : 1][kFwd ? C::kGroups : 1][kFwd ? 128 : 1];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
 
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sm_ring = sm + 2 * kSlot;
-    uint8_t *sm_stat = sm_ring + kStages * kStage;
+    uint8_t *sm_ring = sm + 2 * C::kSlot;
+    uint8_t *sm_stat = sm_ring + C::kStages * C::kStage;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
     if (tid == 0) {
         abort_flag = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.qfull[i], 1);
-            mbar_init(&bars.qempty[i], 1);
+            mbar_init(&bars.qempty[i], C::kRowOps);  // the warps that form scores
             mbar_init(&bars.ofull[i], 1);
-            mbar_init(&bars.ofree[i], 4);
-            mbar_init(&bars.drain[i], 1);
+            mbar_init(&bars.ofree[i], 4 * C::kGroups / (kDkv ? 2 : 1));
         }
-        mbar_init(&bars.drain[2], 1);
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < 4; ++i) mbar_init(&bars.drain[i], 1);
+        for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&bars.full[i], 1);
             mbar_init(&bars.empty[i], 1);
         }
-        for (int i = 0; i < kBufs; ++i) {
-            mbar_init(&bars.sfull[0][i], 1);
-            mbar_init(&bars.sfull[1][i], 1);
-            mbar_init(&bars.pfull[0][i], 4);
-            mbar_init(&bars.pfull[1][i], 4);
-            mbar_init(&bars.bfree[i], 1);
+        for (int i = 0; i < C::kRegions; ++i) {
+            mbar_init(&bars.sfull[i], 1);
+            mbar_init(&bars.wfull[i], 4 * C::kGroups);
+            mbar_init(&bars.sfree[i], kDkv ? 2 : 1);
         }
+        mbar_init(&bars.pfull, 1);
+        mbar_init(&bars.pfree, 4 * C::kGroups);
         fence_mbarrier_init();
     }
-    if (warp == kXScore) {
+    if (warp == C::kS) {
         tmem_alloc(&tmem_base, 512);
         tmem_relinquish();
     }
-    if (warp == kXTma) {
+    if (warp == C::kTma) {
         if (lane == 0) {
-            tma_prefetch_desc(&tm_q);
-            tma_prefetch_desc(&tm_k);
-            tma_prefetch_desc(&tm_v);
+            tma_prefetch_desc(&tm_r0);
+            if (!kFwd) tma_prefetch_desc(&tm_r1);
+            tma_prefetch_desc(&tm_c0);
+            tma_prefetch_desc(&tm_c1);
         }
         __syncwarp();
-        const XRange r = x_range<kCrossFwd>(a.sched, blockIdx.x, gridDim.x, lane);
+        const XRange r = x_range<MODE>(a.sched, blockIdx.x, gridDim.x, lane);
         if (lane == 0) range = r;
     }
     tc_fence_before();
@@ -127,281 +155,359 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     griddep_wait();  // what ran before has ended: memory may be read and written
     const uint32_t tm = tmem_base;
     volatile int *abort = &abort_flag;
-    XIter<kCrossFwd> iter(a.sched, range);
+    XIter<MODE> iter(a.sched, range);
     XItem it;
 
-    if (warp == kXTma) {
+    if (warp == C::kTma) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
-            if (!a.sched.whole) a.pieces[blockIdx.x] = XIter<kCrossFwd>::first(a.sched, range);
+            if (!a.sched.whole) a.pieces[blockIdx.x] = XIter<MODE>::first(a.sched, range);
             int nq = 0, ns = 0;  // items and stages loaded
+            XRing stage;
             bool ok = true;
             while (ok && iter.next(it)) {
                 const int qb = nq & 1;
                 ok = mbar_wait(&bars.qempty[qb], ((nq >> 1) & 1) ^ 1, abort);
                 if (!ok) break;
-                mbar_arrive_expect_tx(&bars.qfull[qb], it.n_tiles * 16384);
-                for (int t = 0; t < it.n_tiles; ++t)
-                    tma_load_3d(sm + qb * kSlot + t * 16384, &tm_q, &bars.qfull[qb], 0, it.r0 + kXTile * t, it.bh);
+                mbar_arrive_expect_tx(&bars.qfull[qb], C::kSlot);
+                tma_load_3d(sm + qb * C::kSlot, &tm_r0, &bars.qfull[qb], 0, it.r0, it.bh);
+                if (!kFwd) tma_load_3d(sm + qb * C::kSlot + 16384, &tm_r1, &bars.qfull[qb], 0, it.r0, it.bh);
                 ++nq;
                 for (int b = 0; b < it.n_blk; ++b) {
-                    const int s = ns % kStages;
-                    ok = mbar_wait(&bars.empty[s], ((ns / kStages) & 1) ^ 1, abort);
+                    const int s = stage.i;
+                    ok = mbar_wait(&bars.empty[s], stage.phase ^ 1, abort);
                     if (!ok) break;
-                    const int col = (it.b0 + b) * kBlk;
-                    uint8_t *dst = sm_ring + s * kStage;
-                    // boxes of 64 keys, the second if it holds a visible one
-                    const int boxes = it.cols - col > 64 ? 2 : 1;
-                    mbar_arrive_expect_tx(&bars.full[s], boxes * 16384);
+                    const int col = (it.b0 + b) * kXCols;
+                    uint8_t *dst = sm_ring + s * C::kStage;
+                    // boxes of 64 columns; of keys, a second one without a visible key is skipped
+                    const int boxes = kDkv || it.cols - col > 64 ? 2 : 1;
+                    mbar_arrive_expect_tx(&bars.full[s], boxes * 16384 + (kDkv ? C::kStat : 0));
                     for (int x = 0; x < boxes; ++x) {
-                        tma_load_3d(dst + x * 8192, &tm_k, &bars.full[s], 0, col + 64 * x, it.bh);
-                        tma_load_3d(dst + kOp + x * 8192, &tm_v, &bars.full[s], 0, col + 64 * x, it.bh);
+                        tma_load_3d(dst + x * 8192, &tm_c0, &bars.full[s], 0, col + 64 * x, it.bh);
+                        tma_load_3d(dst + C::kOp + x * 8192, &tm_c1, &bars.full[s], 0, col + 64 * x, it.bh);
+                    }
+                    if (kDkv) {
+                        const long long o = (long long)it.bh * a.stat_stride + col;
+                        bulk_load(sm_stat + s * C::kStat, a.delta + o, 512, &bars.full[s]);
+                        bulk_load(sm_stat + s * C::kStat + 512, a.rden + o, 512, &bars.full[s]);
                     }
                     ++ns;
+                    stage.next(C::kStages);
                 }
             }
             // every load issued must have landed before the CTA exits
             for (int x = nq > 2 ? nq - 2 : 0; x < nq; ++x) mbar_wait_issued(&bars.qfull[x & 1], (x >> 1) & 1);
-            for (int x = ns > kStages ? ns - kStages : 0; x < ns; ++x)
-                mbar_wait_issued(&bars.full[x % kStages], (x / kStages) & 1);
+            for (int x = ns > C::kStages ? ns - C::kStages : 0; x < ns; ++x)
+                mbar_wait_issued(&bars.full[x % C::kStages], (x / C::kStages) & 1);
         }
-    } else if (warp == kXScore) {
-        // ------------------------------------------------------------ products that form scores
+    } else if (warp == C::kS || warp == C::kP) {
+        // ------------------------------------------------------------ products that form S, P
         if (lane == 0) {
-            const uint32_t id = idesc_bf16(128, kBlk, 0, 0);
-            const uint64_t dR = desc_sw128(smem_u32(sm), 16, 1024);
-            const uint64_t dC = desc_sw128(smem_u32(sm_ring), 16, 1024);
+            const int me = warp - C::kS;
+            const uint32_t id = idesc_bf16(128, 128, 0, 0);
+            const uint64_t dR = desc_sw128(smem_u32(sm + 16384 * me), 16, 1024);
+            const uint64_t dC = desc_sw128(smem_u32(sm_ring + C::kOp * me), 16, 1024);
             const int n_ks = a.d / 16;  // the head's own coordinates: the columns past d are zeros
-            XRing stage, buf;
-            int j = 0, n = 0;  // items, steps
-            // per score buffer (4 bits): the stage + 1 that its current step, of a second tile,
-            // is the last to read, or 0.  A buffer found free releases that stage.
-            uint32_t release = 0;
+            XRing stage, buf;           // buf: S region, or the one of P
+            int j = 0;
+            uint32_t release = 0;  // warp C::kS, per S region (4 bits): the stage + 1 its step reads
             bool ok = true;
             while (ok && iter.next(it)) {
                 const int qb = j & 1;
-                const uint64_t r0 = desc_at(dR, qb * kSlot);
+                const uint64_t r = desc_at(dR, qb * C::kSlot);
                 ok = mbar_wait(&bars.qfull[qb], (j >> 1) & 1, abort);
                 for (int b = 0; b < it.n_blk && ok; ++b) {
-                    const uint64_t c = desc_at(dC, stage.i * kStage);
-                    ok = mbar_wait(&bars.full[stage.i], stage.phase, abort);
-                    for (int t = 0; t < it.n_tiles && ok; ++t, ++n) {
-                        const int x = buf.i;
-                        const uint32_t col = tm + kBuf0 + 128 * x;
-                        const uint64_t r = desc_at(r0, t * 16384);
-                        uint64_t *sfull = &bars.sfull[x_half(it, t, j)][x];
-                        const uint32_t done = (release >> (4 * x)) & 15u;
-                        release = (release & ~(15u << (4 * x))) | ((t == 1 ? stage.i + 1u : 0u) << (4 * x));
-                        ok = mbar_wait(&bars.bfree[x], buf.phase ^ 1, abort);  // the first round passes at once
-                        if (!ok) break;
-                        tc_fence_after();
+                    const uint64_t c = desc_at(dC, stage.i * C::kStage);
+                    const uint32_t col = tm + (me == 0 ? C::kColS + 128 * buf.i : C::kColP);
+                    const uint32_t done = (release >> (4 * buf.i)) & 15u;
+                    release = (release & ~(15u << (4 * buf.i))) | ((stage.i + 1u) << (4 * buf.i));
+                    ok = mbar_wait(&bars.full[stage.i], stage.phase, abort) &&
+                         mbar_wait(me == 0 ? &bars.sfree[buf.i] : &bars.pfree, buf.phase ^ 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            if (ks < n_ks) mma_ss(col, desc_at(r, 32 * ks), desc_at(c, 32 * ks), id, ks > 0);
-                        mma_commit(sfull);
-                        if (done) mbar_arrive(&bars.empty[done - 1]);
-                        buf.next(kBufs);
-                    }
-                    stage.next(kStages);
+                    for (int ks = 0; ks < 4; ++ks)
+                        if (ks < n_ks) mma_ss(col, desc_at(r, 32 * ks), desc_at(c, 32 * ks), id, ks > 0);
+                    mma_commit(me == 0 ? &bars.sfull[buf.i] : &bars.pfull);
+                    // a region found free: every product of the step that used it is done, so
+                    // its stage is (P of that step was formed before its weights)
+                    if (me == 0 && done) mbar_arrive(&bars.empty[done - 1]);
+                    buf.next(me == 0 ? C::kRegions : 1);
+                    stage.next(C::kStages);
                 }
                 if (!ok) break;
                 mma_commit(&bars.qempty[qb]);
                 ++j;
             }
-            mma_commit(&bars.drain[0]);
-            mbar_wait_issued(&bars.drain[0], 0);
+            mma_commit(&bars.drain[me]);
+            mbar_wait_issued(&bars.drain[me], 0);
         }
-    } else if (warp >= kXAcc) {
+    } else if (warp >= C::kAcc) {
         // ------------------------------------------------------------ products that accumulate
-        // One warp per accumulator, so that one's waits and overhead pass while the
-        // other issues, and every accumulator is added to in the order of the steps.
-        if (lane == 0) {
-            const int me = warp - kXAcc;
+        if (lane == 0 && (kDkv || warp == C::kAcc)) {
+            const int me = warp - C::kAcc;  // dkv: 0: dV from w / l and dY, 1: dK from ds and Q
             const uint32_t id = idesc_bf16(128, a.d, 0, 1);  // the head's own columns
-            const uint64_t dV = desc_sw128(smem_u32(sm_ring + kOp), 8192, 1024);
-            const uint32_t acc = tm + 64 * me;
-            XRing stage, buf;
-            uint32_t ophase = 1;  // the accumulator's first use passes at once
-            uint32_t pphase = 0;  // parity of the next of this warp's uses of each buffer
-            int j = 0, n = 0;
+            const uint64_t dC = desc_sw128(smem_u32(sm_ring + (kFwd || (kDkv && me == 0) ? C::kOp : 0)), 8192, 1024);
+            XRing stage, buf, acc;  // acc: forward, dq: the accumulator of the item
+            uint32_t ophase = 1;    // dkv: the accumulator's first use passes at once
             bool ok = true;
             while (ok && iter.next(it)) {
-                const bool mine = it.n_tiles == 2 || (j & 1) == me;
+                const int o = kDkv ? me : acc.i;
+                ok = mbar_wait(&bars.ofree[o], kDkv ? ophase : acc.phase ^ 1, abort);
                 for (int b = 0; b < it.n_blk && ok; ++b) {
-                    const uint64_t c = desc_at(dV, stage.i * kStage);
-                    for (int t = 0; t < it.n_tiles; ++t, ++n) {
-                        if (mine && (it.n_tiles == 1 || t == me)) {
-                            const uint32_t col = tm + kBuf0 + 128 * buf.i;
-                            if (b == 0) {
-                                ok = mbar_wait(&bars.ofree[me], ophase, abort);
-                                if (!ok) break;
-                                ophase ^= 1;
-                            }
-                            ok = mbar_wait(&bars.full[stage.i], stage.phase, abort) &&
-                                 mbar_wait(&bars.pfull[me][buf.i], (pphase >> buf.i) & 1, abort);
-                            if (!ok) break;
-                            pphase ^= 1u << buf.i;
-                            tc_fence_after();
+                    const uint64_t c = desc_at(dC, stage.i * C::kStage);
+                    const uint32_t w = tm + C::kColS + 128 * buf.i + 8 * me;
+                    ok = mbar_wait(&bars.full[stage.i], stage.phase, abort) &&
+                         mbar_wait(&bars.wfull[buf.i], buf.phase, abort);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                            for (int ks = 0; ks < kBlk / 16; ++ks)
-                                mma_ts(acc, col + (SPLIT ? 32 * (ks / 2) + 8 * (ks % 2) : 8 * ks), desc_at(c, 2048 * ks),
-                                       id, b > 0 || ks > 0);
-                            if (SPLIT) {
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ts(tm + 64 * o, w + 16 * ks, desc_at(c, 2048 * ks), id, b > 0 || ks > 0);
+                    if (SPLIT) {
 #pragma unroll
-                                for (int ks = 0; ks < kBlk / 16; ++ks)
-                                    mma_ts(acc, col + 32 * (ks / 2) + 8 * (ks % 2) + 16, desc_at(c, 2048 * ks), id, 1);
-                            }
-                            mma_commit(&bars.bfree[buf.i]);
-                            // an item of one tile, whose steps wait for loads: its stage is free at
-                            // once (with two tiles the scores' warp knows when both are done)
-                            if (it.n_tiles == 1) mma_commit(&bars.empty[stage.i]);
-                            if (b == it.n_blk - 1) mma_commit(&bars.ofull[me]);
-                        }
-                        buf.next(kBufs);
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_ts(tm + 64 * o, w + 16 * ks + 8, desc_at(c, 2048 * ks), id, 1);
                     }
-                    stage.next(kStages);
+                    mma_commit(&bars.sfree[buf.i]);
+                    buf.next(C::kRegions);
+                    stage.next(C::kStages);
                 }
-                ++j;
+                if (!ok) break;
+                mma_commit(&bars.ofull[o]);
+                ophase ^= 1;
+                acc.next(2);
             }
-            mma_commit(&bars.drain[1 + me]);
-            mbar_wait_issued(&bars.drain[1 + me], 0);
+            mma_commit(&bars.drain[2 + me]);
+            mbar_wait_issued(&bars.drain[2 + me], 0);
         }
     } else {
         // ------------------------------------------------------------ weights and epilogue
-        const int half = warp / 4, qd = warp % 4;
+        const int grp = warp / 4, qd = warp % 4;
         const int row = 32 * qd + lane;
         const uint32_t lane_base = static_cast<uint32_t>(32 * qd) << 16;
-        const uint32_t acc = tm + 64 * half + lane_base;
         const int rows = a.sched.rows;
-        int j = 0, ns = 0, n = 0;
-        uint32_t uses = 0, sphase = 0;  // sphase: parity of this half's next use of each buffer
+        const uint32_t tP = tm + C::kColP + C::kCols * grp + lane_base;
+        XRing stage, buf, acc;
+        uint32_t pphase = 0, ophase = 0;
         bool ok = true;
-        zero_dead_rows<kCrossFwd>(a, warp, 8, lane);
+        zero_dead_rows<MODE>(a, warp, 4 * C::kGroups, lane);
         __syncwarp();
         while (ok && iter.next(it)) {
-            // the tile this half takes, if any
-            const int t = it.n_tiles == 2 ? half : (j & 1) == half ? 0 : -1;
-            const int r = it.r0 + kXTile * t + row;
-            const long long gr = (long long)it.bh * rows + r;
-            float l = 0.f;
-            for (int b = t < 0 ? it.n_blk : 0; b < it.n_blk && ok; ++b) {
-                const int m = n + b * it.n_tiles + t;
-                const int x = m % kBufs, s = (ns + b) % kStages;
-                const uint32_t fpar = ((ns + b) / kStages) & 1;
-                const uint32_t buf = tm + kBuf0 + 128 * x + lane_base;
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars.sfull[half][x], (sphase >> x) & 1, abort));
+            const int r = it.r0 + row;
+            const long long gr = (long long)it.bh * rows + r, gs = (long long)it.bh * a.stat_stride + r;
+            const float ndelta = MODE == kCrossDq && r < rows ? a.delta[gs] : 0.f;
+            const uint64_t nd = f32x2_pack(__float_as_uint(ndelta), __float_as_uint(ndelta));
+            float l = 0.f;  // forward: this group's share of the row's weights
+            for (int b = 0; b < it.n_blk; ++b) {
+                const int s = stage.i;
+                const uint32_t tS = tm + C::kColS + 128 * buf.i + C::kCols * grp + lane_base;
+                // of this group's columns, those visible (dkv masks none)
+                const int lim = it.cols - (it.b0 + b) * kXCols - C::kCols * grp;
+                if constexpr (kDkv) {
+                    // the block's -D and 1 / l (zeros past the last query)
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars.full[s], stage.phase, abort));
+                    if (!ok) break;
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars.sfull[buf.i], buf.phase, abort) &&
+                                                 (kFwd || mbar_wait(&bars.pfull, pphase, abort)));
                 if (!ok) break;
-                sphase ^= 1u << x;
                 tc_fence_after();
-                const int lim = it.cols - (it.b0 + b) * kBlk;  // columns below lim are visible
-                uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
-                if constexpr (SPLIT) {
+                if constexpr (kFwd) {
+                    uint32_t v[C::kCols];
+                    static_assert(!kFwd || C::kCols == 32, "one load of 32 columns");
+                    tmem_ld32(tS, v);
+                    tmem_ld_wait();
+                    if (lim < C::kCols) {
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {  // 32 scores: 16 columns of high parts, 16 of low ones
-                        uint32_t v[32], p[16];
-                        tmem_ld32(buf + 32 * h, v);
+                        for (int y = 0; y < C::kCols; ++y) v[y] = y < lim ? v[y] : 0u;
+                    }
+                    uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t w[8], e[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            const uint64_t s2 = f32x2_pack(v[16 * h + 2 * y], v[16 * h + 2 * y + 1]);
+                            const uint64_t w2 = f32x2_mul(s2, s2);
+                            w[y] = f32x2_to_bf16x2(w2);
+                            uint64_t p2 = w2;
+                            if (EXACT) p2 = f32x2_pack(w[y] << 16, w[y] & 0xFFFF0000u);
+                            if (SPLIT) {
+                                e[y] = f32x2_to_bf16x2(f32x2_add(w2, p2 ^ 0x8000000080000000ull));
+                                p2 = f32x2_add(p2, f32x2_pack(e[y] << 16, e[y] & 0xFFFF0000u));
+                            }
+                            sum[y & 1] = f32x2_add(sum[y & 1], p2);
+                        }
+                        tmem_st8(tS + 16 * h, w);
+                        if (SPLIT) tmem_st8(tS + 16 * h + 8, e);
+                    }
+                    const uint64_t z = f32x2_add(sum[0], sum[1]);
+                    l += f32x2_lo(z) + f32x2_hi(z);
+                } else if constexpr (kDkv) {
+                    // Fragment layout: -D and 1 / l of 8 queries serve the thread's 4 rows.  (One
+                    // row per thread would read all 32 columns' of each from shared memory.)
+                    static_assert(!kDkv || C::kCols == 32, "fragment loads of 32 columns");
+                    const float2 *sd = reinterpret_cast<const float2 *>(sm_stat + s * C::kStat) +
+                                       (C::kCols * grp) / 2 + lane % 4;
+                    // P first, all of it: the next step's may then be formed under this one's arithmetic
+                    uint32_t g[32];
+                    tmem_ld_16x256b_x4(tP, g);
+                    tmem_ld_16x256b_x4(tP + (16u << 16), g + 16);
+                    tmem_ld_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.pfree);
+                    float2 fd[4], fr[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        fd[j] = sd[4 * j];
+                        fr[j] = sd[64 + 4 * j];
+                    }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {  // lanes 0 .. 15, 16 .. 31
+                        const uint32_t tSu = tS + (static_cast<uint32_t>(16 * u) << 16);
+                        uint32_t v[16];
+                        tmem_ld_16x256b_x4(tSu, v);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) v[y] = 32 * h + y < lim ? v[y] : 0u;
+                        for (int h = 0; h < 2; ++h) {  // 16 columns: 8 of w / l, 8 of ds / 2
+                            uint32_t w[4], e[4];
 #pragma unroll
-                        for (int y = 0; y < 16; ++y) {
-                            const uint64_t s2 = f32x2_pack(v[2 * y], v[2 * y + 1]), w2 = f32x2_mul(s2, s2);
-                            p[y] = f32x2_to_bf16x2(w2);
-                            const uint64_t hi = f32x2_pack(p[y] << 16, p[y] & 0xFFFF0000u);
-                            const uint32_t q = f32x2_to_bf16x2(f32x2_add(w2, hi ^ 0x8000000080000000ull));
-                            v[y] = q;
-                            acc2[y & 3] = f32x2_add(acc2[y & 3], f32x2_add(hi, f32x2_pack(q << 16, q & 0xFFFF0000u)));
+                            for (int y = 0; y < 4; ++y) {
+                                const int j = 2 * h + y / 2, c = 8 * h + 2 * y;
+                                const uint64_t s2 = f32x2_pack(v[c], v[c + 1]);
+                                const uint64_t g2 = f32x2_pack(g[16 * u + c], g[16 * u + c + 1]);
+                                const uint64_t d2 = f32x2_pack(__float_as_uint(fd[j].x), __float_as_uint(fd[j].y));
+                                const uint64_t r2 = f32x2_pack(__float_as_uint(fr[j].x), __float_as_uint(fr[j].y));
+                                const uint64_t sr2 = f32x2_mul(s2, r2);
+                                w[y] = f32x2_to_bf16x2(f32x2_mul(s2, sr2));
+                                e[y] = f32x2_to_bf16x2(f32x2_mul(sr2, f32x2_add(g2, d2)));
+                            }
+                            tmem_st_16x128b_x2(tSu + 16 * h, w);
+                            tmem_st_16x128b_x2(tSu + 16 * h + 8, e);
                         }
-                        tmem_st16(buf + 32 * h, p);
-                        tmem_st16(buf + 32 * h + 16, v);
                     }
-                } else
+                } else {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[64], p[32];
-                    tmem_ld32(buf + 64 * h, v);
-                    tmem_ld32(buf + 64 * h + 32, v + 32);
-                    tmem_ld_wait();
-                    if (lim < 128) {
+                    for (int h = 0; h < C::kCols / 16; ++h) {
+                        uint32_t v[16], g[16], w[8];
+                        tmem_ld16(tP + 16 * h, g);
+                        tmem_ld16(tS + 16 * h, v);
+                        tmem_ld_wait();
+                        if (h == C::kCols / 16 - 1) {  // P is read: the next step's may be formed
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bars.pfree);
+                        }
+                        if (lim < C::kCols) {
 #pragma unroll
-                        for (int y = 0; y < 64; ++y) v[y] = 64 * h + y < lim ? v[y] : 0u;
+                            for (int y = 0; y < 16; ++y) {
+                                v[y] = 16 * h + y < lim ? v[y] : 0u;
+                                g[y] = 16 * h + y < lim ? g[y] : 0u;
+                            }
+                        }
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            w[y] = f32x2_to_bf16x2(f32x2_mul(f32x2_pack(v[2 * y], v[2 * y + 1]),
+                                                             f32x2_add(f32x2_pack(g[2 * y], g[2 * y + 1]), nd)));
+                        tmem_st8(tS + 16 * h, w);
                     }
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) {
-                        const uint64_t s2 = f32x2_pack(v[2 * y], v[2 * y + 1]);
-                        p[y] = f32x2_to_bf16x2(f32x2_mul(s2, s2));
-                        acc2[y & 3] = f32x2_add(acc2[y & 3], f32x2_pack(p[y] << 16, p[y] & 0xFFFF0000u));
-                    }
-                    tmem_st32(buf + 32 * h, p);
                 }
-                const uint64_t z = f32x2_add(f32x2_add(acc2[0], acc2[1]), f32x2_add(acc2[2], acc2[3]));
-                l += f32x2_lo(z) + f32x2_hi(z);
-                // Values past the visible keys may be anything (NaN times a zero weight is
-                // NaN): cleared in the block where the visible keys end, by every warp of
-                // both halves before it hands its weights over.
-                if (lim < kBlk) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bars.full[s], fpar, abort));
+                // keys (forward: values) past the visible ones may be anything (NaN times a zero
+                // weight is NaN): cleared in the block where the visible keys end
+                if (!kDkv && lim < C::kCols) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars.full[s], stage.phase, abort));
                     if (!ok) break;
-                    uint8_t *op = sm_ring + s * kStage + kOp;
-                    for (int k = lim + qd; k < kBlk; k += 4)
+                    uint8_t *op = sm_ring + s * C::kStage + (kFwd ? C::kOp : 0) + C::kCols * grp * 128;
+                    for (int k = max(lim, 0) + qd; k < C::kCols; k += 4)
                         *reinterpret_cast<uint32_t *>(op + k * 128 + lane * 4) = 0u;
                     fence_proxy_async_smem();
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.pfull[half][x]);
+                if (lane == 0) mbar_arrive(&bars.wfull[buf.i]);
+                pphase ^= 1;
+                buf.next(C::kRegions);
+                stage.next(C::kStages);
             }
             if (!ok) break;
-            if (t >= 0) {
-                uint32_t o[64];
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars.ofull[half], uses & 1, abort));
-                if (!ok) break;
-                ++uses;
-                tc_fence_after();
-                tmem_ld32(acc, o);
-                tmem_ld32(acc + 32, o + 32);
-                tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.ofree[half]);
-                if (r < rows) {
-                    if (it.part >= 0) {  // cut item: the row of the piece's slot
-                        const long long pr = x_part_row(a.sched, it.part) + kXTile * t + row;
-                        store_part(a.part + pr * a.d, o, a.d);
-                        a.part_l[pr] = l;
-                    } else {
-                        store_row(a.o0 + gr * a.d, a.y ? a.y + gr * a.d : nullptr, o, cross_recip(l), a.d);
-                        if (a.den) a.den[gr] = l;
-                    }
-                }
-                __syncwarp();
+            if constexpr (kFwd) {  // the groups' shares; the item after the next writes this buffer again
+                lsum[acc.i][grp][row] = l;
+                asm volatile("bar.sync 1, %0;" ::"n"(128 * C::kGroups) : "memory");
+                l = 0.f;
+#pragma unroll
+                for (int x = 0; x < C::kGroups; ++x) l += lsum[acc.i][x][row];
             }
-            n += it.n_blk * it.n_tiles;
-            ns += it.n_blk;
-            ++j;
+            // this group's columns of the item's accumulators: forward, dq: 64 / groups of
+            // them; dkv: the first groups dV's, the others dK's
+            constexpr int N = kDkv ? 128 / C::kGroups : 64 / C::kGroups;
+            const int ob = kDkv ? grp / (C::kGroups / 2) : acc.i;
+            const int c0 = kDkv ? N * (grp % (C::kGroups / 2)) : N * grp;
+            uint32_t o[64];
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars.ofull[ob], kDkv ? ophase : acc.phase, abort));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < N; c += 16) tmem_ld16(tm + 64 * ob + c0 + c + lane_base, o + c);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.ofree[ob]);
+            if (kDkv && r >= it.live) {  // keys past the visible ones, whatever they hold
+#pragma unroll
+                for (int c = 0; c < N; ++c) o[c] = 0u;
+            }
+            if (r < rows && c0 < a.d) {
+                const int nc = min(N, a.d - c0);
+                if (it.part >= 0) {  // cut item: the row of the piece's slot (dkv: dv's rows, then dk's)
+                    const long long pr = x_part_row(a.sched, it.part) + row + (kDkv ? kXTile * ob : 0);
+                    store_part(a.part + pr * a.d + c0, o, nc);
+                    if (kFwd && grp == 0) a.part_l[pr] = l;
+                } else if (kFwd) {
+                    store_row(a.o0 + gr * a.d + c0, a.y ? a.y + gr * a.d + c0 : nullptr, o, cross_recip(l), nc);
+                    if (a.den && grp == 0) a.den[gr] = l;
+                } else {
+                    const float f = !kDkv ? 2.f * a.rden[gs] : ob ? 2.f : 1.f;
+                    store_row((kDkv && ob ? a.o1 : a.o0) + gr * a.d + c0, nullptr, o, f, nc);
+                }
+            }
+            __syncwarp();
+            ophase ^= 1;
+            acc.next(2);
         }
     }
 
     tc_fence_before();
     __syncthreads();
-    if (warp == kXScore) tmem_dealloc(tm, 512);
+    if (warp == C::kS) tmem_dealloc(tm, 512);
     if (tid == 0 && abort_flag) atomicCAS(a.status, 0, (int)KATA_ERR_TIMEOUT);
+}
+
+template <int MODE, bool SPLIT, bool EXACT>
+cudaError_t launch_mode(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    XLaunch x;
+    cudaError_t e = x_launch(static_cast<CrossMode>(MODE), p, io, x);
+    if (e != cudaSuccess) return e;
+    if ((e = smem_opt_in_once<cross_tc_kernel<MODE, SPLIT, EXACT>>(XCfg<MODE>::kSmem)) != cudaSuccess) return e;
+    ProfScope prof(MODE == kCrossFwd ? "cross_fwd" : MODE == kCrossDq ? "cross_dq" : "cross_dkv", st);
+    if (MODE == kCrossFwd) {  // the call's first kernel
+        cross_tc_kernel<MODE, SPLIT, EXACT><<<x.a.sched.grid, XCfg<MODE>::kThreads, XCfg<MODE>::kSmem, st>>>(
+            x.maps[0], x.maps[1], x.maps[2], x.maps[3], x.a);
+        return cudaGetLastError();
+    }
+    return launch_dependent(cross_tc_kernel<MODE, SPLIT, EXACT>, dim3(x.a.sched.grid), (unsigned)XCfg<MODE>::kThreads,
+                            XCfg<MODE>::kSmem, st, x.maps[0], x.maps[1], x.maps[2], x.maps[3], x.a);
 }
 
 }  // namespace
 
-cudaError_t launch_cross_fwd_tc(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
-    XLaunch x;
-    cudaError_t e = x_launch(kCrossFwd, p, io, x);
-    if (e != cudaSuccess) return e;
-    const bool split = io.y && p.d <= 32;
-    e = split ? smem_opt_in_once<cross_fwd_kernel<true>>(kSmem) : smem_opt_in_once<cross_fwd_kernel<false>>(kSmem);
-    if (e != cudaSuccess) return e;
-    auto *kernel = split ? cross_fwd_kernel<true> : cross_fwd_kernel<false>;
-    ProfScope prof("cross_fwd", st);
-    kernel<<<x.a.sched.grid, kXThreads, kSmem, st>>>(x.maps[0], x.maps[2], x.maps[3], x.a);
-    return cudaGetLastError();
+cudaError_t launch_cross_tc(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    if (mode == kCrossDq) return launch_mode<kCrossDq, false, false>(p, io, st);
+    if (mode == kCrossDkv) return launch_mode<kCrossDkv, false, false>(p, io, st);
+    if (!io.y) return launch_mode<kCrossFwd, false, false>(p, io, st);
+    return p.d <= 32 ? launch_mode<kCrossFwd, true, true>(p, io, st) : launch_mode<kCrossFwd, false, true>(p, io, st);
 }
 
 }  // namespace kata

@@ -1,5 +1,5 @@
-// Parts that the tensor-core kernels of cross attention share (cross_tc.cu, forward;
-// cross_tc_bwd.cu, backward).
+// Parts of the tensor-core kernel of cross attention (cross_tc.cu): arguments, tensor
+// maps, and what reads and writes rows.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -12,8 +12,6 @@
 namespace kata {
 
 using namespace kata::sm100;
-
-constexpr int kXTile = 128;  // rows of a tile
 
 // Place in a ring and the parity of its current round.
 struct XRing {

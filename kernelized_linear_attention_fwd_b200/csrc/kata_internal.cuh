@@ -277,8 +277,7 @@ constexpr int kFewRows = 4;
 // CTAs per SM of that kernel for this many rows (64, 80, 128 registers a thread).
 __host__ __device__ constexpr int few_per_sm(int rows) { return rows == 1 ? 4 : rows == 2 ? 3 : 2; }
 cudaError_t launch_cross_few(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
-cudaError_t launch_cross_fwd_tc(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
-cudaError_t launch_cross_bwd_tc(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
+cudaError_t launch_cross_tc(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 cudaError_t launch_cross_simt(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 // Rows per CTA of the fp32 kernels.
 int cross_simt_rows(CrossMode mode, const CrossPlan &p);

@@ -160,14 +160,12 @@ int cross_splits(long long items, long long steps, int min_steps) {
 //   more than the steps saved), or 16 and more of them per SM;
 // - whole = 1: equal lengths and whole items, dealt evenly, that leave the busiest SM at
 //   most 3% above the average.  (Lengths that differ put stretches of whole items up
-//   to an item apart: 64 sequences of 1501 keys and less, 16 heads, one query: 64 us
-//   against %RAG% us cut.)
+//   to an item apart.)
 bool cross_sched(const CrossPlan &p, CrossMode m, int rows, int cols, XSched &s) {
-    const long long tiles = (rows + 127) / 128, tpi = cross_tc_tiles(m);
-    const long long blocks = (cols + kXCols - 1) / kXCols;
-    const long long items = p.BH * ((tiles + tpi - 1) / tpi);
-    if (items >= (1LL << 31) || p.BH > (1LL << 62) / tiles / blocks) return false;
-    const long long units = p.BH * tiles * blocks;
+    const long long tiles = (rows + kXTile - 1) / kXTile, blocks = (cols + kXCols - 1) / kXCols;
+    const long long items = p.BH * tiles;
+    if (items >= (1LL << 31) || items > (1LL << 62) / blocks) return false;
+    const long long units = items * blocks;
     s.B = p.B;
     s.Hkv = p.Hkv;
     s.rows = rows;
@@ -177,12 +175,12 @@ bool cross_sched(const CrossPlan &p, CrossMode m, int rows, int cols, XSched &s)
     // CTAs that run at a time, and the fewest units worth one
     const int full = m == kCrossFwd && p.few ? few_per_sm(p.R) * kPlanSms : kPlanSms, least = m == kCrossFwd && p.few ? 2 : 4;
     const long long rounds = (items + full - 1) / full;
-    const bool tiny = items < full && blocks * tpi <= least;
+    const bool tiny = items < full && blocks <= least;
     s.whole = tiny || items >= 16 * full ? 2 : rounds * full * 100 <= items * 103 ? 1 : 0;
     s.min_share = s.whole == 2 ? 1 : least;
     const long long most = s.whole == 2 ? items : (units + least - 1) / least;
     s.grid = (int)(most < full ? most : full);
-    const int most_rows = m == kCrossDq ? 128 : 256;  // forward: two tiles; dkv: dv's 128 rows and dk's
+    const int most_rows = m == kCrossDkv ? 256 : 128;  // dkv: dv's 128 rows and dk's
     s.slot_rows = m != kCrossDkv && rows < most_rows ? rows : most_rows;
     return true;
 }
