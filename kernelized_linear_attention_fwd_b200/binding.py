@@ -689,6 +689,8 @@ _I64x3 = ctypes.c_int64 * 3
 
 def _is(t, name, shape, dtype, device):
     """`t` is a contiguous tensor of `shape`, `dtype` on the CUDA device `device`."""
+    if t is None:
+        raise KataError(KATA_ERR_INVALID_ARG, f"{name} is required")
     if not (t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()):
         _check(t, name, shape, dtype, device)
 
