@@ -22,12 +22,13 @@
 // depend on order.
 //
 // Roundings to bf16: the weights (and ds) that go back into the tensor cores as
-// operands, once each.  In the forward of a training step (EXACT) the denominator sums
-// the rounded weights, so that y is a convex combination of values to fp32: with one
-// visible key y = v and, D being formed from the same y, the gradient of q and k is
-// zero up to fp32 rounding instead of up to bf16 rounding.  Without y_out it sums them
-// unrounded, which leaves half of the arithmetic (8192 queries, 16384 keys, 8 heads:
-// 265 us against 295), and the output is within its own rounding of the same.
+// operands, once each.  The denominator is the product of the same rounded weights
+// with a column of ones, in 16 columns more of the product with the values (which
+// the 128-row operand's read pays for anyway), so that y is a convex combination of
+// values to fp32: with one visible key y = v and, D being formed from the same y,
+// the gradient of q and k is zero up to fp32 rounding instead of up to bf16
+// rounding.  (Summing the rounded weights in the warps cost 265 -> 295 us at 8192
+// queries, 16384 keys, 8 heads; this, unrounded ones included, %ONES%.)
 //
 // Schedule.  The work is a line of units, one per (128-row tile, column block),
 // sequence by sequence; every CTA of the persistent grid takes an equal stretch
@@ -37,8 +38,8 @@
 //
 // A step is one tile against one block.  Tensor memory holds
 //
-//   0 .. 127       accumulators: forward, dq: two of 64 columns, items in turn;
-//                  dkv: dV and dK
+//   0 .. 127       accumulators: forward: O and l; dq: two of 64 columns, items in
+//                  turn; dkv: dV and dK
 //   128, 256       S of successive steps (forward: and 384); the weights replace it:
 //                  per 16 scores 8 columns of w (SPLIT: and 8 of low parts), of ds, or
 //                  of w / l and 8 of ds
@@ -71,7 +72,8 @@ struct XCfg {
     static constexpr int kStage = 2 * kOp;
     static constexpr int kStages = kFwd ? 5 : 4;
     static constexpr int kStat = kDkv ? 1024 : 0;  // -D and 1 / l of the block's queries
-    static constexpr int kSmem = 2 * kSlot + kStages * (kStage + kStat) + 1024;
+    static constexpr int kOnes = kFwd ? 16384 : 0;  // a 128 x 64 operand of ones
+    static constexpr int kSmem = 2 * kSlot + kStages * (kStage + kStat) + kOnes + 1024;
     // tensor memory: accumulators in columns 0 .. 127, regions of S, the one of P
     static constexpr int kRegions = kFwd ? 3 : 2;
     static constexpr uint32_t kColS = 128, kColP = 384;
@@ -93,7 +95,7 @@ struct XBars {
 // relative to exact, rms, without and with (0.00166 of it the output's rounding):
 // d = 16 0.0026, 0.0025; d = 32 0.0025, 0.0024; d = 64 0.0024, 0.0024.  For d = 64 it
 // would take the forward of 2048 queries on 4096 keys half as long again.
-template <int MODE, bool SPLIT, bool EXACT>
+template <int MODE, bool SPLIT>
 __global__ void __launch_bounds__(XCfg<MODE>::kThreads, 1)
 cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant__ CUtensorMap tm_r1,
                  const __grid_constant__ CUtensorMap tm_c0, const __grid_constant__ CUtensorMap tm_c1,
@@ -103,15 +105,18 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
     extern __shared__ uint8_t smem_raw[];
     __shared__ XBars<MODE> bars;
     __shared__ XRange range;
-    __shared__ float lsum[kFwd ? 2 : 1][kFwd ? C::kGroups : 1][kFwd ? 128 : 1];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
 
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sm_ring = sm + 2 * C::kSlot;
-    uint8_t *sm_stat = sm_ring + C::kStages * C::kStage;
+    uint8_t *sm_stat = sm_ring + C::kStages * C::kStage, *sm_ones = sm_stat;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
+    if (kFwd) {
+        for (int x = tid; x < C::kOnes / 4; x += C::kThreads) reinterpret_cast<uint32_t *>(sm_ones)[x] = 0x3F803F80u;
+        fence_proxy_async_smem();
+    }
     if (tid == 0) {
         abort_flag = 0;
         for (int i = 0; i < 2; ++i) {
@@ -246,16 +251,21 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
         // ------------------------------------------------------------ products that accumulate
         if (lane == 0 && (kDkv || warp == C::kAcc)) {
             const int me = warp - C::kAcc;  // dkv: 0: dV from w / l and dY, 1: dK from ds and Q
-            const uint32_t id = idesc_bf16(128, a.d, 0, 1);  // the head's own columns
-            const uint64_t dC = desc_sw128(smem_u32(sm_ring + (kFwd || (kDkv && me == 0) ? C::kOp : 0)), 8192, 1024);
-            XRing stage, buf, acc;  // acc: forward, dq: the accumulator of the item
-            uint32_t ophase = 1;    // dkv: the accumulator's first use passes at once
+            // the head's own columns; forward: the block's values and, 64 columns on, ones, whose
+            // product with the weights is the denominator
+            const uint32_t id = idesc_bf16(128, kFwd ? 80 : a.d, 0, 1);
+            const uint8_t *op = sm_ring + (kFwd || (kDkv && me == 0) ? C::kOp : 0);
+            const uint64_t dC = desc_sw128(smem_u32(op), kFwd ? smem_u32(sm_ones) - smem_u32(op) : 8192, 1024);
+            XRing stage, buf, acc;  // acc: dq: the accumulator of the item
+            uint32_t ophase = 1;    // forward, dkv: the accumulator's first use passes at once
             bool ok = true;
             while (ok && iter.next(it)) {
-                const int o = kDkv ? me : acc.i;
-                ok = mbar_wait(&bars.ofree[o], kDkv ? ophase : acc.phase ^ 1, abort);
+                const int o = MODE == kCrossDq ? acc.i : me;
+                ok = mbar_wait(&bars.ofree[o], MODE == kCrossDq ? acc.phase ^ 1 : ophase, abort);
                 for (int b = 0; b < it.n_blk && ok; ++b) {
-                    const uint64_t c = desc_at(dC, stage.i * C::kStage);
+                    uint64_t c = desc_at(dC, stage.i * C::kStage);
+                    // the ones stay where they are: the distance to them shrinks
+                    if (kFwd) c -= static_cast<uint64_t>((stage.i * C::kStage) >> 4) << 16;
                     const uint32_t w = tm + C::kColS + 128 * buf.i + 8 * me;
                     ok = mbar_wait(&bars.full[stage.i], stage.phase, abort) &&
                          mbar_wait(&bars.wfull[buf.i], buf.phase, abort);
@@ -298,7 +308,6 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
             const long long gr = (long long)it.bh * rows + r, gs = (long long)it.bh * a.stat_stride + r;
             const float ndelta = MODE == kCrossDq && r < rows ? a.delta[gs] : 0.f;
             const uint64_t nd = f32x2_pack(__float_as_uint(ndelta), __float_as_uint(ndelta));
-            float l = 0.f;  // forward: this group's share of the row's weights
             for (int b = 0; b < it.n_blk; ++b) {
                 const int s = stage.i;
                 const uint32_t tS = tm + C::kColS + 128 * buf.i + C::kCols * grp + lane_base;
@@ -322,7 +331,6 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
 #pragma unroll
                         for (int y = 0; y < C::kCols; ++y) v[y] = y < lim ? v[y] : 0u;
                     }
-                    uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t w[8], e[8];
@@ -331,19 +339,13 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
                             const uint64_t s2 = f32x2_pack(v[16 * h + 2 * y], v[16 * h + 2 * y + 1]);
                             const uint64_t w2 = f32x2_mul(s2, s2);
                             w[y] = f32x2_to_bf16x2(w2);
-                            uint64_t p2 = w2;
-                            if (EXACT) p2 = f32x2_pack(w[y] << 16, w[y] & 0xFFFF0000u);
-                            if (SPLIT) {
-                                e[y] = f32x2_to_bf16x2(f32x2_add(w2, p2 ^ 0x8000000080000000ull));
-                                p2 = f32x2_add(p2, f32x2_pack(e[y] << 16, e[y] & 0xFFFF0000u));
-                            }
-                            sum[y & 1] = f32x2_add(sum[y & 1], p2);
+                            if (SPLIT)
+                                e[y] = f32x2_to_bf16x2(
+                                    f32x2_add(w2, f32x2_pack(w[y] << 16, w[y] & 0xFFFF0000u) ^ 0x8000000080000000ull));
                         }
                         tmem_st8(tS + 16 * h, w);
                         if (SPLIT) tmem_st8(tS + 16 * h + 8, e);
                     }
-                    const uint64_t z = f32x2_add(sum[0], sum[1]);
-                    l += f32x2_lo(z) + f32x2_hi(z);
                 } else if constexpr (kDkv) {
                     // Fragment layout: -D and 1 / l of 8 queries serve the thread's 4 rows.  (One
                     // row per thread would read all 32 columns' of each from shared memory.)
@@ -433,25 +435,21 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
                 stage.next(C::kStages);
             }
             if (!ok) break;
-            if constexpr (kFwd) {  // the groups' shares; the item after the next writes this buffer again
-                lsum[acc.i][grp][row] = l;
-                asm volatile("bar.sync 1, %0;" ::"n"(128 * C::kGroups) : "memory");
-                l = 0.f;
-#pragma unroll
-                for (int x = 0; x < C::kGroups; ++x) l += lsum[acc.i][x][row];
-            }
             // this group's columns of the item's accumulators: forward, dq: 64 / groups of
             // them; dkv: the first groups dV's, the others dK's
             constexpr int N = kDkv ? 128 / C::kGroups : 64 / C::kGroups;
-            const int ob = kDkv ? grp / (C::kGroups / 2) : acc.i;
+            const int ob = kDkv ? grp / (C::kGroups / 2) : kFwd ? 0 : acc.i;
             const int c0 = kDkv ? N * (grp % (C::kGroups / 2)) : N * grp;
             uint32_t o[64];
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars.ofull[ob], kDkv ? ophase : acc.phase, abort));
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars.ofull[ob], MODE == kCrossDq ? acc.phase : ophase, abort));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < N; c += 16) tmem_ld16(tm + 64 * ob + c0 + c + lane_base, o + c);
+            uint32_t den[8];  // forward: the denominator, in each of the 16 columns from 64 on
+            if (kFwd) tmem_ld8(tm + 64 + lane_base, den);
             tmem_ld_wait();
+            const float l = kFwd ? __uint_as_float(den[0]) : 0.f;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.ofree[ob]);
@@ -485,29 +483,28 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
     if (tid == 0 && abort_flag) atomicCAS(a.status, 0, (int)KATA_ERR_TIMEOUT);
 }
 
-template <int MODE, bool SPLIT, bool EXACT>
+template <int MODE, bool SPLIT>
 cudaError_t launch_mode(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     XLaunch x;
     cudaError_t e = x_launch(static_cast<CrossMode>(MODE), p, io, x);
     if (e != cudaSuccess) return e;
-    if ((e = smem_opt_in_once<cross_tc_kernel<MODE, SPLIT, EXACT>>(XCfg<MODE>::kSmem)) != cudaSuccess) return e;
+    if ((e = smem_opt_in_once<cross_tc_kernel<MODE, SPLIT>>(XCfg<MODE>::kSmem)) != cudaSuccess) return e;
     ProfScope prof(MODE == kCrossFwd ? "cross_fwd" : MODE == kCrossDq ? "cross_dq" : "cross_dkv", st);
     if (MODE == kCrossFwd) {  // the call's first kernel
-        cross_tc_kernel<MODE, SPLIT, EXACT><<<x.a.sched.grid, XCfg<MODE>::kThreads, XCfg<MODE>::kSmem, st>>>(
+        cross_tc_kernel<MODE, SPLIT><<<x.a.sched.grid, XCfg<MODE>::kThreads, XCfg<MODE>::kSmem, st>>>(
             x.maps[0], x.maps[1], x.maps[2], x.maps[3], x.a);
         return cudaGetLastError();
     }
-    return launch_dependent(cross_tc_kernel<MODE, SPLIT, EXACT>, dim3(x.a.sched.grid), (unsigned)XCfg<MODE>::kThreads,
+    return launch_dependent(cross_tc_kernel<MODE, SPLIT>, dim3(x.a.sched.grid), (unsigned)XCfg<MODE>::kThreads,
                             XCfg<MODE>::kSmem, st, x.maps[0], x.maps[1], x.maps[2], x.maps[3], x.a);
 }
 
 }  // namespace
 
 cudaError_t launch_cross_tc(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
-    if (mode == kCrossDq) return launch_mode<kCrossDq, false, false>(p, io, st);
-    if (mode == kCrossDkv) return launch_mode<kCrossDkv, false, false>(p, io, st);
-    if (!io.y) return launch_mode<kCrossFwd, false, false>(p, io, st);
-    return p.d <= 32 ? launch_mode<kCrossFwd, true, true>(p, io, st) : launch_mode<kCrossFwd, false, true>(p, io, st);
+    if (mode == kCrossDq) return launch_mode<kCrossDq, false>(p, io, st);
+    if (mode == kCrossDkv) return launch_mode<kCrossDkv, false>(p, io, st);
+    return io.y && p.d <= 32 ? launch_mode<kCrossFwd, true>(p, io, st) : launch_mode<kCrossFwd, false>(p, io, st);
 }
 
 }  // namespace kata
