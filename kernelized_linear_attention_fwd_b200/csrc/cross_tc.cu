@@ -62,7 +62,7 @@ template <int MODE>
 struct XCfg {
     static constexpr bool kFwd = MODE == kCrossFwd, kDkv = MODE == kCrossDkv;
     // groups of 4 warps that turn scores into weights, and the other warps behind them
-    static constexpr int kGroups = MODE == kCrossDq ? 2 : 4;
+    static constexpr int kGroups = MODE == kCrossDkv ? 4 : 2;
     static constexpr int kTma = 4 * kGroups, kS = kTma + 1, kP = kFwd ? -1 : kTma + 2, kAcc = kTma + (kFwd ? 2 : 3);
     static constexpr int kThreads = 32 * (kFwd ? kAcc + 1 : kAcc + 2);
     static constexpr int kCols = kXCols / kGroups;  // columns of a step that a group turns
@@ -323,28 +323,30 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
                 if (!ok) break;
                 tc_fence_after();
                 if constexpr (kFwd) {
-                    uint32_t v[C::kCols];
-                    static_assert(!kFwd || C::kCols == 32, "one load of 32 columns");
-                    tmem_ld32(tS, v);
-                    tmem_ld_wait();
-                    if (lim < C::kCols) {
 #pragma unroll
-                        for (int y = 0; y < C::kCols; ++y) v[y] = y < lim ? v[y] : 0u;
-                    }
+                    for (int g = 0; g < C::kCols / 32; ++g) {
+                        uint32_t v[32];
+                        tmem_ld32(tS + 32 * g, v);
+                        tmem_ld_wait();
+                        if (lim < C::kCols) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t w[8], e[8];
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            const uint64_t s2 = f32x2_pack(v[16 * h + 2 * y], v[16 * h + 2 * y + 1]);
-                            const uint64_t w2 = f32x2_mul(s2, s2);
-                            w[y] = f32x2_to_bf16x2(w2);
-                            if (SPLIT)
-                                e[y] = f32x2_to_bf16x2(
-                                    f32x2_add(w2, f32x2_pack(w[y] << 16, w[y] & 0xFFFF0000u) ^ 0x8000000080000000ull));
+                            for (int y = 0; y < 32; ++y) v[y] = 32 * g + y < lim ? v[y] : 0u;
                         }
-                        tmem_st8(tS + 16 * h, w);
-                        if (SPLIT) tmem_st8(tS + 16 * h + 8, e);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t w[8], e[8];
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) {
+                                const uint64_t s2 = f32x2_pack(v[16 * h + 2 * y], v[16 * h + 2 * y + 1]);
+                                const uint64_t w2 = f32x2_mul(s2, s2);
+                                w[y] = f32x2_to_bf16x2(w2);
+                                if (SPLIT)
+                                    e[y] = f32x2_to_bf16x2(f32x2_add(
+                                        w2, f32x2_pack(w[y] << 16, w[y] & 0xFFFF0000u) ^ 0x8000000080000000ull));
+                            }
+                            tmem_st8(tS + 32 * g + 16 * h, w);
+                            if (SPLIT) tmem_st8(tS + 32 * g + 16 * h + 8, e);
+                        }
                     }
                 } else if constexpr (kDkv) {
                     // Fragment layout: -D and 1 / l of 8 queries serve the thread's 4 rows.  (One
