@@ -267,7 +267,9 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
                     // the ones stay where they are: the distance to them shrinks
                     if (kFwd) c -= static_cast<uint64_t>((stage.i * C::kStage) >> 4) << 16;
                     const uint32_t w = tm + C::kColS + 128 * buf.i + 8 * me;
-                    ok = mbar_wait(&bars.full[stage.i], stage.phase, abort) &&
+                    // that the stage has landed is the warps' wait in the forward, whose steps this
+                    // warp bounds (256 us here, 245 there), and this warp's in dq and dkv
+                    ok = (kFwd || mbar_wait(&bars.full[stage.i], stage.phase, abort)) &&
                          mbar_wait(&bars.wfull[buf.i], buf.phase, abort);
                     if (!ok) break;
                     tc_fence_after();
@@ -431,7 +433,12 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.wfull[buf.i]);
+                if (lane == 0) {
+                    if (kFwd) ok = mbar_wait(&bars.full[s], stage.phase, abort);
+                    if (ok) mbar_arrive(&bars.wfull[buf.i]);
+                }
+                if (kFwd) ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (kFwd && !ok) break;
                 pphase ^= 1;
                 buf.next(C::kRegions);
                 stage.next(C::kStages);
