@@ -83,8 +83,9 @@ template <int MODE>
 struct XBars {
     using C = XCfg<MODE>;
     uint64_t qfull[2], qempty[2], full[C::kStages], empty[C::kStages];
-    // per S region: scores formed, weights stored, products done; P formed, P read
-    uint64_t sfull[C::kRegions], wfull[C::kRegions], sfree[C::kRegions], pfull, pfree;
+    // per S region: scores formed (S and P of the step), weights stored, products done;
+    // P read
+    uint64_t sfull[C::kRegions], wfull[C::kRegions], sfree[C::kRegions], pfree;
     uint64_t ofull[2], ofree[2], drain[4];
 };
 
@@ -131,11 +132,10 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
             mbar_init(&bars.empty[i], 1);
         }
         for (int i = 0; i < C::kRegions; ++i) {
-            mbar_init(&bars.sfull[i], 1);
+            mbar_init(&bars.sfull[i], C::kRowOps);
             mbar_init(&bars.wfull[i], 4 * C::kGroups);
             mbar_init(&bars.sfree[i], kDkv ? 2 : 1);
         }
-        mbar_init(&bars.pfull, 1);
         mbar_init(&bars.pfree, 4 * C::kGroups);
         fence_mbarrier_init();
     }
@@ -213,7 +213,8 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
             const uint64_t dR = desc_sw128(smem_u32(sm + 16384 * me), 16, 1024);
             const uint64_t dC = desc_sw128(smem_u32(sm_ring + C::kOp * me), 16, 1024);
             const int n_ks = a.d / 16;  // the head's own coordinates: the columns past d are zeros
-            XRing stage, buf;           // buf: S region, or the one of P
+            XRing stage, buf;           // buf: the step's S region
+            uint32_t pphase = 1;        // P's region: the first use passes at once
             int j = 0;
             uint32_t release = 0;  // warp C::kS, per S region (4 bits): the stage + 1 its step reads
             bool ok = true;
@@ -227,17 +228,19 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
                     const uint32_t done = (release >> (4 * buf.i)) & 15u;
                     release = (release & ~(15u << (4 * buf.i))) | ((stage.i + 1u) << (4 * buf.i));
                     ok = mbar_wait(&bars.full[stage.i], stage.phase, abort) &&
-                         mbar_wait(me == 0 ? &bars.sfree[buf.i] : &bars.pfree, buf.phase ^ 1, abort);
+                         (me == 0 ? mbar_wait(&bars.sfree[buf.i], buf.phase ^ 1, abort)
+                                  : mbar_wait(&bars.pfree, pphase, abort));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         if (ks < n_ks) mma_ss(col, desc_at(r, 32 * ks), desc_at(c, 32 * ks), id, ks > 0);
-                    mma_commit(me == 0 ? &bars.sfull[buf.i] : &bars.pfull);
+                    mma_commit(&bars.sfull[buf.i]);
                     // a region found free: every product of the step that used it is done, so
                     // its stage is (P of that step was formed before its weights)
                     if (me == 0 && done) mbar_arrive(&bars.empty[done - 1]);
-                    buf.next(me == 0 ? C::kRegions : 1);
+                    buf.next(C::kRegions);
+                    pphase ^= 1;
                     stage.next(C::kStages);
                 }
                 if (!ok) break;
@@ -301,7 +304,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
         const int rows = a.sched.rows;
         const uint32_t tP = tm + C::kColP + C::kCols * grp + lane_base;
         XRing stage, buf, acc;
-        uint32_t pphase = 0, ophase = 0;
+        uint32_t ophase = 0;
         bool ok = true;
         zero_dead_rows<MODE>(a, warp, 4 * C::kGroups, lane);
         __syncwarp();
@@ -320,8 +323,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
                     ok = __all_sync(0xffffffffu, mbar_wait(&bars.full[s], stage.phase, abort));
                     if (!ok) break;
                 }
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars.sfull[buf.i], buf.phase, abort) &&
-                                                 (kFwd || mbar_wait(&bars.pfull, pphase, abort)));
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars.sfull[buf.i], buf.phase, abort));
                 if (!ok) break;
                 tc_fence_after();
                 if constexpr (kFwd) {
@@ -439,7 +441,6 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
                 }
                 if (kFwd) ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (kFwd && !ok) break;
-                pphase ^= 1;
                 buf.next(C::kRegions);
                 stage.next(C::kStages);
             }
