@@ -1,4 +1,4 @@
-// Cross attention: the steps around the main kernels (cross_tc.cu, cross_simt.cu)
+// Cross attention: the steps around the main kernels (cross_tc.cu, cross_f32.cu)
 // that both types share: the backward pass's row statistics, and the joins of
 // partial sums when a long axis was split over several CTAs.
 #include <cuda_bf16.h>
@@ -243,7 +243,7 @@ cudaError_t launch_cut_join(const CrossPlan &p, const CrossIo &io, cudaStream_t 
 
 cudaError_t launch_main(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     if (mode == kCrossFwd && p.few) return launch_cross_few(p, io, st);
-    if (p.dtype != KATA_BF16) return launch_cross_simt(mode, p, io, st);
+    if (p.dtype != KATA_BF16) return launch_cross_f32(mode, p, io, st);
     return launch_cross_tc(mode, p, io, st);
 }
 

@@ -230,7 +230,8 @@ struct NormRotate {
 dim3 norm_rotate_grid(const NormRotate &p);
 cudaError_t launch_norm_rotate(const NormRotate &p, cudaStream_t st);
 
-// Cross attention (cross_tc.cu for bf16, cross_simt.cu for fp32).  The query
+// Cross attention (cross_tc.cu for bf16, cross_f32.cu for fp32, cross_few.cu for few
+// rows).  The query
 // heads that share a key head are consecutive in memory, so they are the rows of
 // one problem: BH = B Hkv problems of R = (H / Hkv) Tq rows and Tk keys.
 enum CrossMode : int { kCrossFwd = 0, kCrossDq = 1, kCrossDkv = 2 };
@@ -272,15 +273,15 @@ inline int cross_whole(const XSched &s, const CrossIo &io) { return s.whole == 2
 cudaError_t launch_cross_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 cudaError_t launch_cross_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 // One mode's main kernel: forward of at most kFewRows rows per key head; others in
-// bf16 on the tensor cores, in fp32 on the CUDA cores.
+// bf16 and in fp32.
 constexpr int kFewRows = 4;
 // CTAs per SM of that kernel for this many rows (64, 80, 128 registers a thread).
 __host__ __device__ constexpr int few_per_sm(int rows) { return rows == 1 ? 4 : rows == 2 ? 3 : 2; }
 cudaError_t launch_cross_few(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 cudaError_t launch_cross_tc(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
-cudaError_t launch_cross_simt(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
-// Rows per CTA of the fp32 kernels.
-int cross_simt_rows(CrossMode mode, const CrossPlan &p);
+cudaError_t launch_cross_f32(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
+// Rows of a CTA and columns of a block of the fp32 kernels.
+constexpr int kF32Tile = 64;
 
 // Keys that sequence b may attend to: its length, within [0, Tk].
 __device__ __forceinline__ int cross_length(const int *key_lengths, int b, int Tk) {

@@ -146,13 +146,13 @@ bool hits_inputs(const NormRotate &p, const void *o, size_t n) {
 // ---------------------------------------------------------------------------
 // Cross attention
 // ---------------------------------------------------------------------------
-// Pieces of the summed axis: 1 when the items fill the SMs, else as many as give
-// every SM one item, each of at least min_steps steps of the kernel.
-int cross_splits(long long items, long long steps, int min_steps) {
-    if (items >= kPlanSms) return 1;
-    long long s = kPlanSms / items;
-    if (s > steps / min_steps) s = steps / min_steps;
-    return s < 1 ? 1 : (int)s;
+// fp32: pieces of the summed axis: 1 when the items fill the SMs (two at a time on
+// each), else as many as do, each of at least one block.
+int cross_splits(long long items, long long blocks) {
+    if (items >= 2 * kPlanSms) return 1;
+    long long s = 2 * kPlanSms / items;
+    if (s > blocks) s = blocks;
+    return (int)((blocks + (blocks + s - 1) / s - 1) / ((blocks + s - 1) / s));  // none of them empty
 }
 
 // The tensor cores' schedule of one mode.  Items are cut unless that gains little:
@@ -216,10 +216,9 @@ kata_status cross_plan(int B, int H, int Hkv, int Tq, int Tk, int d, kata_dtype 
             part_rows = p.sched[m].whole == 2 ? 0 : (size_t)p.sched[m].grid * 2 * p.sched[m].slot_rows;
             p.splits[m] = 1;
         } else {
-            const int t = cross_simt_rows(m, p);
-            const long long items = p.BH * ((n + t - 1) / t);
+            const long long items = p.BH * ((n + kF32Tile - 1) / kF32Tile);
             if (items >= most) return KATA_ERR_UNSUPPORTED;
-            p.splits[m] = cross_splits(items, (c + 63) / 64, 2);
+            p.splits[m] = cross_splits(items, (c + kF32Tile - 1) / kF32Tile);
             if (p.splits[m] > 1) part_rows = (size_t)p.splits[m] * p.BH * n * (m == kCrossDkv ? 2 : 1);
         }
         const size_t part = align_up(part_rows * d * 4);
