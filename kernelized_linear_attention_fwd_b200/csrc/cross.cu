@@ -70,6 +70,7 @@ cross_join_kernel(const float *part, const float *part_l, const float *rden, T *
     constexpr int kRows = 16 / G;
     __shared__ float4 red[16][16];
     __shared__ float red_l[16];
+    sm100::griddep_wait();
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, g = ty % G, c = 4 * tx;
     const long long row = (long long)blockIdx.x * kRows + ty / G;
     const bool on = row < n_rows;
@@ -127,13 +128,10 @@ cudaError_t launch_join(const CrossPlan &p, CrossMode mode, const float *part, c
                         long long split_stride, cudaStream_t st) {
     const int s = p.splits[mode];
     ProfScope prof("cross_join", st);
-    if (s > 8)
-        cross_join_kernel<T, JOIN, 16><<<(unsigned)n_rows, 256, 0, st>>>(
-            part, part_l, rden, static_cast<T *>(out), y, den, n_rows, split_stride, s, p.R, p.R_pad, p.d);
-    else
-        cross_join_kernel<T, JOIN, 1><<<(unsigned)((n_rows + 15) / 16), 256, 0, st>>>(
-            part, part_l, rden, static_cast<T *>(out), y, den, n_rows, split_stride, s, p.R, p.R_pad, p.d);
-    return cudaGetLastError();
+    const bool many = s > 8;
+    return launch_dependent(many ? cross_join_kernel<T, JOIN, 16> : cross_join_kernel<T, JOIN, 1>,
+                            dim3((unsigned)(many ? n_rows : (n_rows + 15) / 16)), 256u, 0, st, part, part_l, rden,
+                            static_cast<T *>(out), y, den, n_rows, split_stride, s, p.R, p.R_pad, p.d);
 }
 
 // Joins the items that the schedule of the tensor cores and of few rows cut (cross_sched.cuh).  Grid x: the

@@ -193,6 +193,7 @@ template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 2)
 cross_f32_kernel(const FArgs a) {
     extern __shared__ __align__(128) uint8_t sm[];
+    griddep_wait();
     uint8_t *R0 = sm, *R1 = R0 + kOperand;  // R1: backward only
     uint8_t *C0 = R0 + (MODE == kCrossFwd ? 1 : 2) * kOperand, *C1 = C0 + kOperand;
     float *sd = reinterpret_cast<float *>(C1 + kOperand), *sr = sd + kN;  // dkv only
@@ -339,7 +340,10 @@ cudaError_t launch_one(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     const cudaError_t e = smem_opt_in_once<cross_f32_kernel<D, MODE>>(smem);
     if (e != cudaSuccess) return e;
     ProfScope prof(MODE == kCrossFwd ? "cross_fwd_f32" : MODE == kCrossDq ? "cross_dq_f32" : "cross_dkv_f32", st);
-    cross_f32_kernel<D, MODE><<<(unsigned)(p.BH * a.tiles * a.splits), kThreads, smem, st>>>(a);
+    const dim3 grid((unsigned)(p.BH * a.tiles * a.splits));
+    if (MODE != kCrossFwd)
+        return launch_dependent(cross_f32_kernel<D, MODE>, grid, (unsigned)kThreads, smem, st, a);
+    cross_f32_kernel<D, MODE><<<grid, kThreads, smem, st>>>(a);  // the call's first kernel
     return cudaGetLastError();
 }
 

@@ -146,13 +146,23 @@ bool hits_inputs(const NormRotate &p, const void *o, size_t n) {
 // ---------------------------------------------------------------------------
 // Cross attention
 // ---------------------------------------------------------------------------
-// fp32: pieces of the summed axis: 1 when the items fill the SMs (two at a time on
-// each), else as many as do, each of at least one block.
+// fp32: pieces of the summed axis, none empty: 1 when the items fill the SMs, else the
+// number that gives the busiest SM the least to do, counting a block as 1, what a CTA
+// does besides its blocks (loading its rows, storing its sums) as 1, and two CTAs that
+// share an SM as 1.3 times one (4096 queries and keys, one head: one CTA an SM 111 us,
+// two 85).
 int cross_splits(long long items, long long blocks) {
     if (items >= 2 * kPlanSms) return 1;
-    long long s = 2 * kPlanSms / items;
-    if (s > blocks) s = blocks;
-    return (int)((blocks + (blocks + s - 1) / s - 1) / ((blocks + s - 1) / s));  // none of them empty
+    long long best = 1, best_cost = 0;
+    for (long long piece = blocks; piece >= 1; piece = piece > 64 ? piece - piece / 16 : piece - 1) {
+        const long long s = (blocks + piece - 1) / piece;
+        const long long n = (items * s + kPlanSms - 1) / kPlanSms, cost = (n / 2 * 13 + n % 2 * 10) * (piece + 1);
+        if (best_cost == 0 || cost < best_cost) {
+            best = s;
+            best_cost = cost;
+        }
+    }
+    return (int)best;
 }
 
 // The tensor cores' schedule of one mode.  Items are cut unless that gains little:
