@@ -58,19 +58,26 @@ cross_stats_kernel(const T *dout, const float *y, const float *den, float *delta
     }
 }
 
-// Joins the pieces of a row: sum over splits in order, by G groups of 16 threads
-// each (thread = 4 columns), then the groups in order.  kJoinDen: divided by the
-// summed denominators (forward; y and den exported if given); kJoinRow: times
+// The joins of the fp32 kernels' pieces.  Sum over splits in order, by G groups of 16
+// threads each (thread = 4 columns), then the groups in order.  kJoinDen: divided by
+// the summed denominators (forward; y and den exported if given); kJoinRow: times
 // 2 / l of the row (dq); kJoinPlain: as is (dk, dv).
 enum Join { kJoinDen, kJoinRow, kJoinPlain };
-template <typename T, int JOIN, int G>
-__global__ void __launch_bounds__(256)
-cross_join_kernel(const float *part, const float *part_l, const float *rden, T *out, float *y, float *den,
-                  long long n_rows, long long split_stride, int splits, int R, int R_pad, int d) {
+struct SplitJob {
+    const float *part, *part_l, *rden;
+    float *out, *y, *den;
+    long long n_rows, split_stride;
+    int splits, R, R_pad, d;
+};
+template <int JOIN, int G>
+__device__ void split_join(const SplitJob &j) {
+    const float *part = j.part, *part_l = j.part_l, *rden = j.rden;
+    float *out = j.out, *y = j.y, *den = j.den;
+    const long long n_rows = j.n_rows, split_stride = j.split_stride;
+    const int splits = j.splits, R = j.R, R_pad = j.R_pad, d = j.d;
     constexpr int kRows = 16 / G;
     __shared__ float4 red[16][16];
     __shared__ float red_l[16];
-    sm100::griddep_wait();
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, g = ty % G, c = 4 * tx;
     const long long row = (long long)blockIdx.x * kRows + ty / G;
     const bool on = row < n_rows;
@@ -112,43 +119,59 @@ cross_join_kernel(const float *part, const float *part_l, const float *rden, T *
     s.z *= f;
     s.w *= f;
     const long long o = row * d + c;
-    store_out(out, o, s.x);
-    store_out(out, o + 1, s.y);
-    store_out(out, o + 2, s.z);
-    store_out(out, o + 3, s.w);
+    *reinterpret_cast<float4 *>(out + o) = s;
     if (JOIN == kJoinDen) {
         if (y) *reinterpret_cast<float4 *>(y + o) = s;
         if (den && c == 0) den[row] = l;
     }
 }
 
-template <typename T, int JOIN>
-cudaError_t launch_join(const CrossPlan &p, CrossMode mode, const float *part, const float *part_l,
-                        const float *rden, void *out, float *y, float *den, long long n_rows,
-                        long long split_stride, cudaStream_t st) {
-    const int s = p.splits[mode];
-    ProfScope prof("cross_join", st);
-    const bool many = s > 8;
-    return launch_dependent(many ? cross_join_kernel<T, JOIN, 16> : cross_join_kernel<T, JOIN, 1>,
-                            dim3((unsigned)(many ? n_rows : (n_rows + 15) / 16)), 256u, 0, st, part, part_l, rden,
-                            static_cast<T *>(out), y, den, n_rows, split_stride, s, p.R, p.R_pad, p.d);
+template <int G>
+__global__ void __launch_bounds__(256)
+split_join_forward(const SplitJob j) {
+    sm100::griddep_wait();
+    split_join<kJoinDen, G>(j);
 }
+// Grid z: dq, dv, dk (those with one piece are not joined: no rows).
+template <int G>
+__global__ void __launch_bounds__(256)
+split_join_backward(const SplitJob q, const SplitJob v, const SplitJob k) {
+    sm100::griddep_wait();
+    if (blockIdx.z == 0)
+        split_join<kJoinRow, G>(q);
+    else
+        split_join<kJoinPlain, G>(blockIdx.z == 1 ? v : k);
+}
+unsigned split_join_blocks(const SplitJob &j, int G) { return (unsigned)((j.n_rows + 16 / G - 1) / (16 / G)); }
 
-// Joins the items that the schedule of the tensor cores and of few rows cut (cross_sched.cuh).  Grid x: the
-// stretch boundaries c = 1 .. G - 1; the block of the first boundary inside an item
+// Joins the items that the schedule of the tensor cores and of few rows cut
+// (cross_sched.cuh).  Grid x: the stretch boundaries c = 1 .. G - 1; the block of the first boundary inside an item
 // adds the item's pieces in order: the end of CTA c - 1's stretch, then the starts
 // of the later CTAs' up to the item's end, as the CTAs have recorded them.  A block
 // of 256 threads takes 16 / G16 rows (grid y), thread = 4 columns of a row and every
 // G16-th piece.
+template <typename T>
+struct CutJob {
+    XSched s;
+    const XPiece *pieces;
+    const float *part, *part_l, *rden;
+    T *o0, *o1;
+    float *y, *den;
+    int R_pad, d;
+};
 template <typename T, int MODE, int G16>
-__global__ void __launch_bounds__(256)
-cross_cut_join_kernel(const XSched s, const XPiece *pieces, const float *part, const float *part_l, const float *rden,
-                     T *o0, T *o1, float *y, float *den, int grid, int R_pad, int d) {
+__device__ void cut_join(const CutJob<T> &j) {
+    const XSched &s = j.s;
+    const XPiece *pieces = j.pieces;
+    const float *part = j.part, *part_l = j.part_l, *rden = j.rden;
+    T *o0 = j.o0, *o1 = j.o1;
+    float *y = j.y, *den = j.den;
+    const int R_pad = j.R_pad, d = j.d, grid = s.grid;
     constexpr int kRows = 16 / G16;
     __shared__ float4 red[16][16];
     __shared__ float red_l[16];
-    sm100::griddep_wait();
     const int c = blockIdx.x + 1, lane = threadIdx.x % 32;
+    if (c >= grid || (int)blockIdx.y * kRows >= s.slot_rows) return;
     const XPiece me = pieces[c], prev = pieces[c - 1];
     const bool same = prev.bh == me.bh && prev.r0 == me.r0;
     if (me.bh < 0 || !me.cont || (same && prev.cont)) return;
@@ -220,23 +243,65 @@ cross_cut_join_kernel(const XSched s, const XPiece *pieces, const float *part, c
     }
 }
 
-template <typename T, int MODE>
-cudaError_t launch_cut_join(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
-    const XSched &s = p.sched[MODE];
-    if (cross_whole(s, io) || s.grid == 1) return cudaSuccess;
+// G16: as many threads per 4 columns as 16 where an item has few rows and so many
+// pieces.
+template <typename T, int G16>
+__global__ void __launch_bounds__(256)
+cut_join_forward(const CutJob<T> j) {
+    sm100::griddep_wait();
+    cut_join<T, kCrossFwd, G16>(j);
+}
+// Grid z: dq, dkv (grid 1: none cut).
+template <typename T, int G16>
+__global__ void __launch_bounds__(256)
+cut_join_backward(const CutJob<T> q, const CutJob<T> kv) {
+    sm100::griddep_wait();
+    if (blockIdx.z == 0)
+        cut_join<T, kCrossDq, G16>(q);
+    else
+        cut_join<T, kCrossDkv, 1>(kv);
+}
+
+template <typename T>
+CutJob<T> cut_job(CrossMode mode, const CrossPlan &p, const CrossIo &io) {
     char *ws = static_cast<char *>(io.ws);
-    const float *part = reinterpret_cast<const float *>(ws + p.ws_part[MODE]);
-    const float *part_l = reinterpret_cast<const float *>(ws + p.ws_part_l);
-    const float *rden = reinterpret_cast<const float *>(ws + p.ws_rden);
-    T *o0 = static_cast<T *>(MODE == kCrossFwd ? io.out : MODE == kCrossDq ? io.dq : io.dv);
-    T *o1 = static_cast<T *>(io.dk);
-    // few rows: an item is cut into many pieces, which 16 threads share per 4 columns
-    const bool few = s.slot_rows <= 64;
-    const dim3 grid(s.grid - 1, few ? s.slot_rows : (s.slot_rows + 15) / 16);
-    const XPiece *pieces = reinterpret_cast<const XPiece *>(ws + p.ws_pieces[MODE]);
-    ProfScope prof("cross_join", st);
-    return launch_dependent(few ? cross_cut_join_kernel<T, MODE, 16> : cross_cut_join_kernel<T, MODE, 1>, grid, 256u, 0, st, s,
-                            pieces, part, part_l, rden, o0, o1, io.y, io.den, s.grid, p.R_pad, p.d);
+    CutJob<T> j;
+    j.s = p.sched[mode];
+    if (cross_whole(j.s, io)) j.s.grid = 1;  // nothing is cut
+    j.pieces = reinterpret_cast<const XPiece *>(ws + p.ws_pieces[mode]);
+    j.part = reinterpret_cast<const float *>(ws + p.ws_part[mode]);
+    j.part_l = reinterpret_cast<const float *>(ws + p.ws_part_l);
+    j.rden = reinterpret_cast<const float *>(ws + p.ws_rden);
+    j.o0 = static_cast<T *>(mode == kCrossFwd ? io.out : mode == kCrossDq ? io.dq : io.dv);
+    j.o1 = static_cast<T *>(io.dk);
+    j.y = io.y;
+    j.den = io.den;
+    j.R_pad = p.R_pad;
+    j.d = p.d;
+    return j;
+}
+template <typename T>
+dim3 cut_grid(const CutJob<T> &j, bool few) {
+    return dim3(j.s.grid - 1, few ? j.s.slot_rows : (j.s.slot_rows + 15) / 16);
+}
+
+SplitJob split_job(CrossMode mode, const CrossPlan &p, const CrossIo &io) {
+    const char *ws = static_cast<const char *>(io.ws);
+    const long long n = p.BH * (mode == kCrossDkv ? p.Tk : p.R);
+    SplitJob j;
+    j.part = reinterpret_cast<const float *>(ws + p.ws_part[mode]);
+    j.part_l = reinterpret_cast<const float *>(ws + p.ws_part_l);
+    j.rden = reinterpret_cast<const float *>(ws + p.ws_rden);
+    j.out = static_cast<float *>(mode == kCrossFwd ? io.out : mode == kCrossDq ? io.dq : io.dv);
+    j.y = io.y;
+    j.den = io.den;
+    j.splits = p.splits[mode];
+    j.n_rows = j.splits > 1 ? n : 0;
+    j.split_stride = mode == kCrossDkv ? 2 * n : n;
+    j.R = p.R;
+    j.R_pad = p.R_pad;
+    j.d = p.d;
+    return j;
 }
 
 cudaError_t launch_main(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
@@ -247,13 +312,21 @@ cudaError_t launch_main(CrossMode mode, const CrossPlan &p, const CrossIo &io, c
 
 template <typename T>
 cudaError_t forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
-    cudaError_t e = launch_main(kCrossFwd, p, io, st);
-    if (e == cudaSuccess && (p.few || p.dtype == KATA_BF16)) return launch_cut_join<T, kCrossFwd>(p, io, st);
-    if (e != cudaSuccess || p.splits[kCrossFwd] == 1) return e;
-    const char *ws = static_cast<const char *>(io.ws);
-    return launch_join<T, kJoinDen>(p, kCrossFwd, reinterpret_cast<const float *>(ws + p.ws_part[kCrossFwd]),
-                                    reinterpret_cast<const float *>(ws + p.ws_part_l), nullptr, io.out, io.y, io.den,
-                                    p.BH * p.R, p.BH * p.R, st);
+    const cudaError_t e = launch_main(kCrossFwd, p, io, st);
+    if (e != cudaSuccess) return e;
+    ProfScope prof("cross_join", st);
+    if (p.few || p.dtype == KATA_BF16) {
+        const CutJob<T> j = cut_job<T>(kCrossFwd, p, io);
+        if (j.s.grid == 1) return cudaSuccess;
+        const bool few = j.s.slot_rows <= 64;
+        return launch_dependent(few ? cut_join_forward<T, 16> : cut_join_forward<T, 1>, cut_grid(j, few), 256u, 0, st,
+                                j);
+    }
+    const SplitJob j = split_job(kCrossFwd, p, io);
+    if (j.n_rows == 0) return cudaSuccess;
+    const bool many = j.splits > 8;
+    return launch_dependent(many ? split_join_forward<16> : split_join_forward<1>,
+                            dim3(split_join_blocks(j, many ? 16 : 1)), 256u, 0, st, j);
 }
 
 template <typename T>
@@ -269,26 +342,26 @@ cudaError_t backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if ((e = launch_main(kCrossDq, p, io, st)) != cudaSuccess) return e;
-    if (p.dtype == KATA_BF16) {
-        if ((e = launch_cut_join<T, kCrossDq>(p, io, st)) != cudaSuccess) return e;
-        if ((e = launch_main(kCrossDkv, p, io, st)) != cudaSuccess) return e;
-        return launch_cut_join<T, kCrossDkv>(p, io, st);
-    }
-    if (p.splits[kCrossDq] > 1) {
-        e = launch_join<T, kJoinRow>(p, kCrossDq, reinterpret_cast<const float *>(ws + p.ws_part[kCrossDq]), nullptr,
-                                     rden, io.dq, nullptr, nullptr, p.BH * p.R, p.BH * p.R, st);
-        if (e != cudaSuccess) return e;
-    }
     if ((e = launch_main(kCrossDkv, p, io, st)) != cudaSuccess) return e;
-    if (p.splits[kCrossDkv] > 1) {
-        const float *part = reinterpret_cast<const float *>(ws + p.ws_part[kCrossDkv]);
-        const long long n = p.BH * p.Tk;
-        e = launch_join<T, kJoinPlain>(p, kCrossDkv, part, nullptr, nullptr, io.dv, nullptr, nullptr, n, 2 * n, st);
-        if (e != cudaSuccess) return e;
-        e = launch_join<T, kJoinPlain>(p, kCrossDkv, part + n * p.d, nullptr, nullptr, io.dk, nullptr, nullptr, n,
-                                       2 * n, st);
+    ProfScope prof("cross_join", st);
+    if (p.dtype == KATA_BF16) {
+        const CutJob<T> q = cut_job<T>(kCrossDq, p, io), kv = cut_job<T>(kCrossDkv, p, io);
+        const bool few = q.s.slot_rows <= 64;
+        dim3 grid = cut_grid(q, few);
+        const dim3 g = cut_grid(kv, false);
+        if (g.x > 0) grid = dim3(g.x > grid.x ? g.x : grid.x, g.y > grid.y ? g.y : grid.y, 2);
+        if (grid.x == 0) return cudaSuccess;
+        return launch_dependent(few ? cut_join_backward<T, 16> : cut_join_backward<T, 1>, grid, 256u, 0, st, q, kv);
     }
-    return e;
+    const SplitJob q = split_job(kCrossDq, p, io), v = split_job(kCrossDkv, p, io);
+    SplitJob k = v;
+    k.part = v.part + (v.split_stride / 2) * p.d;
+    k.out = static_cast<float *>(io.dk);
+    const int G = q.splits > 8 || v.splits > 8 ? 16 : 1;
+    const unsigned nq = split_join_blocks(q, G), nv = split_join_blocks(v, G);
+    if (nq == 0 && nv == 0) return cudaSuccess;
+    return launch_dependent(G == 16 ? split_join_backward<16> : split_join_backward<1>,
+                            dim3(nq > nv ? nq : nv, 1, nv > 0 ? 3 : 1), 256u, 0, st, q, v, k);
 }
 
 }  // namespace
