@@ -482,8 +482,10 @@ kata_status kata_qk_norm_rotate_backward(
  *          are then split over the SMs and joined.  A decode step is Tq = 1.
  *
  * KATA_BF16 runs on the tensor cores for every d (fp32 accumulation; the weights
- * are rounded to bf16 once, in the numerator and the denominator alike),
- * KATA_F32 in fp32 on the CUDA cores.
+ * are rounded to bf16 once, in the numerator and the denominator alike).  KATA_F32
+ * keeps fp32 accuracy: its products are sums of products of three bf16 numbers per
+ * operand (24 bits).  At most 4 rows per key head ((H / Hkv) * Tq, a decode step)
+ * run in fp32 on the CUDA cores for either type.
  *
  * kata_cross_backward: with dout the gradient of out and D_t = dout_t.y_t,
  *
@@ -497,9 +499,9 @@ kata_status kata_qk_norm_rotate_backward(
  * Workspace: kata_cross_backward_workspace_bytes(...) bytes, 256-byte aligned.
  *
  * The size queries return 0 for arguments that the calls would reject.  Sizes:
- * d in {16, 32, 64}; (H / Hkv) * Tq below 2^31 - 256 and the number of work items
- * (256 rows, or 16 in fp32, of one key head) below 2^31, else
- * KATA_ERR_UNSUPPORTED.
+ * d in {16, 32, 64}; (H / Hkv) * Tq and Tk below 2^31 - 256, B * Hkv times either at
+ * most 2^40, and the number of work items (128 rows, in fp32 64, of one key head)
+ * below 2^31, else KATA_ERR_UNSUPPORTED.
  */
 size_t kata_cross_forward_workspace_bytes(int B, int H, int Hkv, int Tq, int Tk, int d,
                                           kata_dtype dtype);

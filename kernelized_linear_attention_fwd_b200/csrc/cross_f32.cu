@@ -10,7 +10,7 @@
 // six products of exact bf16 pairs summed in fp32.  The five small ones come before
 // h h', so that only a block's last few additions round at the sum's own size, and
 // every block's sum is formed on its own and then added to the total in fp32.  Error
-// against exact: %F32ERR%.
+// against exact, rms: 1.5e-7 to 1.9e-7 (the same in plain fp32 products: 2.4e-7).
 //
 // A CTA of 4 warps owns 64 rows and walks the other axis in blocks of 64 columns, whose
 // operands it splits into three planes of shared memory as it loads them.  A warp
@@ -19,7 +19,11 @@
 // The register-level products (mma.sync) suit tiles this small, whose split takes
 // the arithmetic of all the warps: tcgen05 would need the three planes of the
 // weights in tensor memory beside their scores, 192 columns where a step of the bf16
-// kernel has 128.  %F32RATE%
+// kernel has 128.  Measured (8 heads, 2048 queries and keys, d = 64): forward 158 us,
+// dq 220 us, dkv 288 us, which is 54, 58 and 60 TFLOP/s of fp32 products (the CUDA
+// cores' form of this kernel: 279, 394, 521 us, bound by its shared-memory reads);
+// bound by the register-level products, whose pipe is 66 to 74% active at 543
+// TFLOP/s of bf16 products / 6.
 #include <cuda_bf16.h>
 
 #include "kata_internal.cuh"

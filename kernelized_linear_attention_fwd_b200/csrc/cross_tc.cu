@@ -27,8 +27,8 @@
 // the 128-row operand's read pays for anyway), so that y is a convex combination of
 // values to fp32: with one visible key y = v and, D being formed from the same y,
 // the gradient of q and k is zero up to fp32 rounding instead of up to bf16
-// rounding.  (Summing the rounded weights in the warps cost 265 -> 295 us at 8192
-// queries, 16384 keys, 8 heads; this, unrounded ones included, %ONES%.)
+// rounding.  (8192 queries, 16384 keys, 8 heads: 295 us with the rounded weights summed
+// by the warps, 265 us with the unrounded ones, 258 us this way.)
 //
 // Schedule.  The work is a line of units, one per (128-row tile, column block),
 // sequence by sequence; every CTA of the persistent grid takes an equal stretch

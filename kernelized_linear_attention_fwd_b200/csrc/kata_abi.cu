@@ -255,7 +255,7 @@ using kata::overlaps;
 
 extern "C" {
 
-int kata_version(void) { return 100; }
+int kata_version(void) { return 200; }
 
 const char *kata_status_string(kata_status s) {
     switch (s) {

@@ -201,8 +201,12 @@ struct NormArgs {
 };
 
 // A warp loads up to U row groups at a time; what is left of a token's heads goes
-// group by group.  Bound by the loads once the arithmetic is packed (fp32 pairs,
-// gains folded into the angles once per token): %NORM%.
+// group by group.  The arithmetic is packed (fp32 pairs) and the forward's gains are
+// folded into the angles once per token and tensor: 139 us without either for 65536
+// tokens of 16 + 16 heads of 64 (537 MB), 95 us so, 5.7 TB/s.  The gradient (32768
+// tokens of 16 + 4 heads, 252 MB) takes 70 us, 3.6 TB/s: half of its warps' time is
+// waiting for loads, and neither more warps of fewer registers, nor more rows at a
+// time, nor loading a set of rows ahead across tokens changed it (70 to 76 us).
 template <typename T, int D, bool INTER, bool BWD>
 __global__ void __launch_bounds__(32 * kNormWarps, norm_per_sm(BWD))
 norm_rotate_kernel(const NormArgs<T> a) {
