@@ -439,8 +439,9 @@ kata_status kata_decode_step_packed(const void *q, const void *k, const void *v,
  * kata_qk_norm_rotate_backward_workspace_bytes(...) bytes, 256-byte aligned.
  * dq and dk must not overlap any input.
  *
- * Weights, inv_freq: 16-byte aligned like every pointer; B * T * (Hq + Hk) at
- * most 2^40.  Offsets are 64-bit.
+ * Weights, inv_freq: 16-byte aligned like every pointer (positions: 8); B * T *
+ * (Hq + Hk) at most 2^40, T below 2^31 - 2^16, else KATA_ERR_UNSUPPORTED.
+ * Offsets are 64-bit.
  */
 kata_status kata_qk_norm_rotate(const void *q, const void *k, void *q_out, void *k_out,
                                 const float *q_weight, const float *k_weight,
@@ -484,7 +485,8 @@ kata_status kata_qk_norm_rotate_backward(
  * KATA_BF16 runs on the tensor cores for every d (fp32 accumulation; the weights
  * are rounded to bf16 once, in the numerator and the denominator alike).  KATA_F32
  * keeps fp32 accuracy: its products are sums of products of three bf16 numbers per
- * operand (24 bits).  At most 4 rows per key head ((H / Hkv) * Tq, a decode step)
+ * operand (24 bits; for magnitudes between 2^-100 and 2^127, and not-a-number where
+ * an infinity is visible).  At most 4 rows per key head ((H / Hkv) * Tq, a decode step)
  * run in fp32 on the CUDA cores for either type.
  *
  * kata_cross_backward: with dout the gradient of out and D_t = dout_t.y_t,

@@ -82,6 +82,7 @@ struct XLine {
         first = min(s.B, lane * run);
         last = min(s.B, first + run);
         units = 0;
+#pragma unroll 8
         for (int b = first; b < last; ++b) {
             int live, tiles, blocks;
             x_extent<MODE>(s, b, live, tiles, blocks);
