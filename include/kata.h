@@ -503,7 +503,7 @@ kata_status kata_qk_norm_rotate_backward(
  * The size queries return 0 for arguments that the calls would reject.  Sizes:
  * d in {16, 32, 64}; (H / Hkv) * Tq and Tk below 2^31 - 256, B * Hkv times either at
  * most 2^40, and the number of work items (128 rows, in fp32 64, of one key head)
- * below 2^31, else KATA_ERR_UNSUPPORTED.
+ * below 2^31 (fp32: 2^30), else KATA_ERR_UNSUPPORTED.
  */
 size_t kata_cross_forward_workspace_bytes(int B, int H, int Hkv, int Tq, int Tk, int d,
                                           kata_dtype dtype);

@@ -304,15 +304,11 @@ SplitJob split_job(CrossMode mode, const CrossPlan &p, const CrossIo &io) {
     return j;
 }
 
-cudaError_t launch_main(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
-    if (mode == kCrossFwd && p.few) return launch_cross_few(p, io, st);
-    if (p.dtype != KATA_BF16) return launch_cross_f32(mode, p, io, st);
-    return launch_cross_tc(mode, p, io, st);
-}
-
 template <typename T>
 cudaError_t forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
-    const cudaError_t e = launch_main(kCrossFwd, p, io, st);
+    const cudaError_t e = p.few                     ? launch_cross_few(p, io, st)
+                          : p.dtype == KATA_BF16 ? launch_cross_tc(kCrossFwd, p, io, st)
+                                                 : launch_cross_f32_forward(p, io, st);
     if (e != cudaSuccess) return e;
     ProfScope prof("cross_join", st);
     if (p.few || p.dtype == KATA_BF16) {
@@ -341,8 +337,13 @@ cudaError_t backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if ((e = launch_main(kCrossDq, p, io, st)) != cudaSuccess) return e;
-    if ((e = launch_main(kCrossDkv, p, io, st)) != cudaSuccess) return e;
+    if (p.dtype == KATA_BF16) {
+        if ((e = launch_cross_tc(kCrossDq, p, io, st)) != cudaSuccess) return e;
+        e = launch_cross_tc(kCrossDkv, p, io, st);
+    } else {
+        e = launch_cross_f32_backward(p, io, st);
+    }
+    if (e != cudaSuccess) return e;
     ProfScope prof("cross_join", st);
     if (p.dtype == KATA_BF16) {
         const CutJob<T> q = cut_job<T>(kCrossDq, p, io), kv = cut_job<T>(kCrossDkv, p, io);

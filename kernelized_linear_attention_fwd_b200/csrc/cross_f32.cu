@@ -194,17 +194,14 @@ __device__ __forceinline__ void accumulate(float (&acc)[D / 8][4], W w, uint32_t
 }
 
 template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 2)
-cross_f32_kernel(const FArgs a) {
-    extern __shared__ __align__(128) uint8_t sm[];
-    griddep_wait();
+__device__ __forceinline__ void cross_f32(const FArgs &a, int cta, uint8_t *sm) {
     uint8_t *R0 = sm, *R1 = R0 + kOperand;  // R1: backward only
     uint8_t *C0 = R0 + (MODE == kCrossFwd ? 1 : 2) * kOperand, *C1 = C0 + kOperand;
     float *sd = reinterpret_cast<float *>(C1 + kOperand), *sr = sd + kN;  // dkv only
 
     const int lane = threadIdx.x % 32, w0 = threadIdx.x / 32 * 16;  // the warp's first row
     const int g = lane / 4, q = 2 * (lane % 4);                     // fragment row and first column
-    const int split = blockIdx.x % a.splits, x = blockIdx.x / a.splits;
+    const int split = cta % a.splits, x = cta / a.splits;
     const int bh = x / a.tiles, r0 = (x % a.tiles) * kN;
     const int live = cross_length(a.key_lengths, bh / a.Hkv, a.Tk);
     const int rows = MODE == kCrossDkv ? live : a.rows, cols = MODE == kCrossDkv ? a.cols : live;
@@ -313,57 +310,91 @@ cross_f32_kernel(const FArgs a) {
     }
 }
 
-template <int D, int MODE>
-cudaError_t launch_one(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+cross_f32_forward(const FArgs a) {
+    extern __shared__ __align__(128) uint8_t sm[];
+    cross_f32<D, kCrossFwd>(a, blockIdx.x, sm);
+}
+// dq and dkv in one launch, dkv's longer CTAs first: neither needs the other, and the
+// SMs that one leaves idle go to the other.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+cross_f32_backward(const FArgs q, const FArgs kv, int n_kv) {
+    extern __shared__ __align__(128) uint8_t sm[];
+    griddep_wait();
+    if ((int)blockIdx.x < n_kv)
+        cross_f32<D, kCrossDkv>(kv, blockIdx.x, sm);
+    else
+        cross_f32<D, kCrossDq>(q, blockIdx.x - n_kv, sm);
+}
+
+FArgs f32_args(CrossMode mode, const CrossPlan &p, const CrossIo &io) {
     const char *ws = static_cast<const char *>(io.ws);
+    const bool dkv = mode == kCrossDkv;
     auto f = [](const void *x) { return static_cast<const float *>(x); };
     auto w = [&](size_t o) { return reinterpret_cast<float *>(const_cast<char *>(ws) + o); };
     FArgs a{};
-    a.rows = MODE == kCrossDkv ? p.Tk : p.R;
-    a.cols = MODE == kCrossDkv ? p.R : p.Tk;
+    a.rows = dkv ? p.Tk : p.R;
+    a.cols = dkv ? p.R : p.Tk;
     a.Hkv = p.Hkv;
     a.tiles = (a.rows + kN - 1) / kN;
-    a.splits = p.splits[MODE];
+    a.splits = p.splits[mode];
     a.Tk = p.Tk;
     a.stat_stride = p.R_pad;
     a.BH = p.BH;
     a.key_lengths = io.key_lengths;
-    a.r0 = f(MODE == kCrossDkv ? io.k : io.q);
-    a.r1 = f(MODE == kCrossDkv ? io.v : io.dout);
-    a.c0 = f(MODE == kCrossDkv ? io.q : io.k);
-    a.c1 = f(MODE == kCrossDkv ? io.dout : io.v);
-    a.o0 = static_cast<float *>(MODE == kCrossFwd ? io.out : MODE == kCrossDq ? io.dq : io.dv);
+    a.r0 = f(dkv ? io.k : io.q);
+    a.r1 = f(dkv ? io.v : io.dout);
+    a.c0 = f(dkv ? io.q : io.k);
+    a.c1 = f(dkv ? io.dout : io.v);
+    a.o0 = static_cast<float *>(mode == kCrossFwd ? io.out : mode == kCrossDq ? io.dq : io.dv);
     a.o1 = static_cast<float *>(io.dk);
     a.y = io.y;
     a.den = io.den;
-    a.part = w(p.ws_part[MODE]);
+    a.part = w(p.ws_part[mode]);
     a.part_l = w(p.ws_part_l);
     a.delta = w(p.ws_delta);
     a.rden = w(p.ws_rden);
-    constexpr int smem = f32_smem<MODE>();
-    const cudaError_t e = smem_opt_in_once<cross_f32_kernel<D, MODE>>(smem);
-    if (e != cudaSuccess) return e;
-    ProfScope prof(MODE == kCrossFwd ? "cross_fwd_f32" : MODE == kCrossDq ? "cross_dq_f32" : "cross_dkv_f32", st);
-    const dim3 grid((unsigned)(p.BH * a.tiles * a.splits));
-    if (MODE != kCrossFwd)
-        return launch_dependent(cross_f32_kernel<D, MODE>, grid, (unsigned)kThreads, smem, st, a);
-    cross_f32_kernel<D, MODE><<<grid, kThreads, smem, st>>>(a);  // the call's first kernel
-    return cudaGetLastError();
+    return a;
 }
+unsigned f32_grid(const FArgs &a) { return (unsigned)(a.BH * a.tiles * a.splits); }
 
 template <int D>
-cudaError_t launch_d(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
-    if (mode == kCrossDq) return launch_one<D, kCrossDq>(p, io, st);
-    return mode == kCrossDkv ? launch_one<D, kCrossDkv>(p, io, st) : launch_one<D, kCrossFwd>(p, io, st);
+cudaError_t launch_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    const FArgs a = f32_args(kCrossFwd, p, io);
+    constexpr int smem = f32_smem<kCrossFwd>();
+    const cudaError_t e = smem_opt_in_once<cross_f32_forward<D>>(smem);
+    if (e != cudaSuccess) return e;
+    ProfScope prof("cross_fwd_f32", st);
+    cross_f32_forward<D><<<f32_grid(a), kThreads, smem, st>>>(a);  // the call's first kernel
+    return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    const FArgs q = f32_args(kCrossDq, p, io), kv = f32_args(kCrossDkv, p, io);
+    constexpr int smem = f32_smem<kCrossDkv>();
+    const cudaError_t e = smem_opt_in_once<cross_f32_backward<D>>(smem);
+    if (e != cudaSuccess) return e;
+    ProfScope prof("cross_bwd_f32", st);
+    return launch_dependent(cross_f32_backward<D>, dim3(f32_grid(kv) + f32_grid(q)), (unsigned)kThreads, smem, st, q,
+                            kv, (int)f32_grid(kv));
 }
 
 }  // namespace
 
-cudaError_t launch_cross_f32(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+cudaError_t launch_cross_f32_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     switch (p.d) {
-        case 16: return launch_d<16>(mode, p, io, st);
-        case 32: return launch_d<32>(mode, p, io, st);
-        default: return launch_d<64>(mode, p, io, st);
+        case 16: return launch_forward<16>(p, io, st);
+        case 32: return launch_forward<32>(p, io, st);
+        default: return launch_forward<64>(p, io, st);
+    }
+}
+cudaError_t launch_cross_f32_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    switch (p.d) {
+        case 16: return launch_backward<16>(p, io, st);
+        case 32: return launch_backward<32>(p, io, st);
+        default: return launch_backward<64>(p, io, st);
     }
 }
 

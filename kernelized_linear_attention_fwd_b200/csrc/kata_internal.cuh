@@ -279,7 +279,8 @@ constexpr int kFewRows = 4;
 __host__ __device__ constexpr int few_per_sm(int rows) { return rows == 1 ? 4 : rows == 2 ? 3 : 2; }
 cudaError_t launch_cross_few(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 cudaError_t launch_cross_tc(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
-cudaError_t launch_cross_f32(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
+cudaError_t launch_cross_f32_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
+cudaError_t launch_cross_f32_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);  // dq and dkv
 // Rows of a CTA and columns of a block of the fp32 kernels.
 constexpr int kF32Tile = 64;
 

@@ -228,7 +228,7 @@ kata_status cross_plan(int B, int H, int Hkv, int Tq, int Tk, int d, kata_dtype 
             p.splits[m] = 1;
         } else {
             const long long items = p.BH * ((n + kF32Tile - 1) / kF32Tile);
-            if (items >= most) return KATA_ERR_UNSUPPORTED;
+            if (items >= most / 2) return KATA_ERR_UNSUPPORTED;  // dq's and dkv's share a grid
             p.splits[m] = cross_splits(items, (c + kF32Tile - 1) / kF32Tile);
             if (p.splits[m] > 1) part_rows = (size_t)p.splits[m] * p.BH * n * (m == kCrossDkv ? 2 : 1);
         }
