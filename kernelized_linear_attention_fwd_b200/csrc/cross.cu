@@ -307,7 +307,7 @@ SplitJob split_job(CrossMode mode, const CrossPlan &p, const CrossIo &io) {
 template <typename T>
 cudaError_t forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     const cudaError_t e = p.few                     ? launch_cross_few(p, io, st)
-                          : p.dtype == KATA_BF16 ? launch_cross_tc(kCrossFwd, p, io, st)
+                          : p.dtype == KATA_BF16 ? launch_cross_tc_forward(p, io, st)
                                                  : launch_cross_f32_forward(p, io, st);
     if (e != cudaSuccess) return e;
     ProfScope prof("cross_join", st);
@@ -337,12 +337,7 @@ cudaError_t backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (p.dtype == KATA_BF16) {
-        if ((e = launch_cross_tc(kCrossDq, p, io, st)) != cudaSuccess) return e;
-        e = launch_cross_tc(kCrossDkv, p, io, st);
-    } else {
-        e = launch_cross_f32_backward(p, io, st);
-    }
+    e = p.dtype == KATA_BF16 ? launch_cross_tc_backward(p, io, st) : launch_cross_f32_backward(p, io, st);
     if (e != cudaSuccess) return e;
     ProfScope prof("cross_join", st);
     if (p.dtype == KATA_BF16) {

@@ -68,7 +68,7 @@ cross_few_kernel(const FArgs a) {
     __shared__ float red[kFWarps][RB][D], red_l[kFWarps][RB];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, key = lane / L, c = 8 * (lane % L);
     if (warp == 0) {
-        const XRange r = x_range<kCrossFwd>(a.sched, blockIdx.x, gridDim.x, lane);
+        const XRange r = x_range<kCrossFwd>(a.sched, blockIdx.x, lane);
         if (lane == 0) range = r;
     }
     __syncthreads();
@@ -84,7 +84,7 @@ cross_few_kernel(const FArgs a) {
                 if (a.den && x < rows) a.den[bh * rows + x] = 0.f;
             }
         }
-    XIter<kCrossFwd> iter(a.sched, range);
+    XIter<kCrossFwd> iter(a.sched, range, blockIdx.x);
     XItem it;
     while (iter.next(it)) {
         const T *kp = static_cast<const T *>(a.k) + (long long)it.bh * a.sched.cols * D + c;

@@ -140,9 +140,9 @@ struct XLine {
 
 // CTA c's stretch.  All 32 lanes.
 template <int MODE>
-__device__ __forceinline__ XRange x_range(const XSched &s, int c, int grid, int lane) {
+__device__ __forceinline__ XRange x_range(const XSched &s, int c, int lane) {
     const XLine<MODE> line(s, lane);
-    const long long n = line.share(s, grid);
+    const long long n = line.share(s, s.grid);
     XRange r;
     r.from = line.place(s, n * c);
     r.to = line.place(s, n * (c + 1));
@@ -153,13 +153,14 @@ template <int MODE>
 struct XIter {
     const XSched &s;
     XPos at, to;
-    int pieces = 0;
+    int cta, pieces = 0;
 
-    __device__ __forceinline__ XIter(const XSched &s_, const XRange &r) : s(s_), at(r.from), to(r.to) {}
+    __device__ __forceinline__ XIter(const XSched &s_, const XRange &r, int cta_)
+        : s(s_), at(r.from), to(r.to), cta(cta_) {}
 
     // The first piece, of an iterator that has not started (bh = -1: none).
     __device__ __forceinline__ static XPiece first(const XSched &s, const XRange &r) {
-        XIter x(s, r);
+        XIter x(s, r, 0);
         XItem it;
         if (!x.next(it)) return {-1, 0, 0, 0};
         return {it.bh, it.r0, it.b0 > 0, it.reaches_end};
@@ -183,7 +184,7 @@ struct XIter {
             it.cols = MODE == kCrossDkv ? s.cols : live;
             it.live = live;
             it.reaches_end = end == blocks;
-            it.part = at.blk == 0 && end == blocks ? -1 : 2 * (int)blockIdx.x + (pieces ? 1 : 0);
+            it.part = at.blk == 0 && end == blocks ? -1 : 2 * cta + (pieces ? 1 : 0);
             ++pieces;
             if (cut) {
                 at.blk = end;

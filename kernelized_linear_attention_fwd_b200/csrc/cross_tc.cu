@@ -52,17 +52,18 @@
 // long).  One warp loads (TMA), one issues S, one P, one or two (dkv) accumulate.
 // 16 warps turn scores into weights, 32 columns each of their 32 rows (dkv with 8 warps
 // of 64 columns took 207 us where 16 take 189: 4 sequences of 16 heads, 2048 queries,
-// 4096 keys, ragged); dq, with half of dkv's arithmetic, has 8 (143 us; 16: 147).
+// 4096 keys, ragged); dq, with half of dkv's arithmetic, has 8 (143 us; 16: 147), and the
+// forward, with a quarter, 8 (256 us; 16: 258).
 #include "cross_tc.cuh"
 
 namespace kata {
 namespace {
 
-template <int MODE>
+// GROUPS: of 4 warps that turn scores into weights; the other warps come behind them.
+template <int MODE, int GROUPS>
 struct XCfg {
     static constexpr bool kFwd = MODE == kCrossFwd, kDkv = MODE == kCrossDkv;
-    // groups of 4 warps that turn scores into weights, and the other warps behind them
-    static constexpr int kGroups = MODE == kCrossDkv ? 4 : 2;
+    static constexpr int kGroups = GROUPS;
     static constexpr int kTma = 4 * kGroups, kS = kTma + 1, kP = kFwd ? -1 : kTma + 2, kAcc = kTma + (kFwd ? 2 : 3);
     static constexpr int kThreads = 32 * (kFwd ? kAcc + 1 : kAcc + 2);
     static constexpr int kCols = kXCols / kGroups;  // columns of a step that a group turns
@@ -79,9 +80,8 @@ struct XCfg {
     static constexpr uint32_t kColS = 128, kColP = 384;
 };
 
-template <int MODE>
+template <typename C>
 struct XBars {
-    using C = XCfg<MODE>;
     uint64_t qfull[2], qempty[2], full[C::kStages], empty[C::kStages];
     // per S region: scores formed (S and P of the step), weights stored, products done;
     // P read
@@ -96,15 +96,13 @@ struct XBars {
 // relative to exact, rms, without and with (0.00166 of it the output's rounding):
 // d = 16 0.0026, 0.0025; d = 32 0.0025, 0.0024; d = 64 0.0024, 0.0024.  For d = 64 it
 // would take the forward of 2048 queries on 4096 keys half as long again.
-template <int MODE, bool SPLIT>
-__global__ void __launch_bounds__(XCfg<MODE>::kThreads, 1)
-cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant__ CUtensorMap tm_r1,
-                 const __grid_constant__ CUtensorMap tm_c0, const __grid_constant__ CUtensorMap tm_c1,
-                 const XArgs a) {
-    using C = XCfg<MODE>;
+template <int MODE, int GROUPS, bool SPLIT>
+__device__ __forceinline__ void cross_tc(const CUtensorMap &tm_r0, const CUtensorMap &tm_r1, const CUtensorMap &tm_c0,
+                                         const CUtensorMap &tm_c1, const XArgs &a, int cta) {
+    using C = XCfg<MODE, GROUPS>;
     constexpr bool kFwd = C::kFwd, kDkv = C::kDkv;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ XBars<MODE> bars;
+    __shared__ XBars<C> bars;
     __shared__ XRange range;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -151,7 +149,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
             tma_prefetch_desc(&tm_c1);
         }
         __syncwarp();
-        const XRange r = x_range<MODE>(a.sched, blockIdx.x, gridDim.x, lane);
+        const XRange r = x_range<MODE>(a.sched, cta, lane);
         if (lane == 0) range = r;
     }
     tc_fence_before();
@@ -160,13 +158,13 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
     griddep_wait();  // what ran before has ended: memory may be read and written
     const uint32_t tm = tmem_base;
     volatile int *abort = &abort_flag;
-    XIter<MODE> iter(a.sched, range);
+    XIter<MODE> iter(a.sched, range, cta);
     XItem it;
 
     if (warp == C::kTma) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
-            if (!a.sched.whole) a.pieces[blockIdx.x] = XIter<MODE>::first(a.sched, range);
+            if (!a.sched.whole) a.pieces[cta] = XIter<MODE>::first(a.sched, range);
             int nq = 0, ns = 0;  // items and stages loaded
             XRing stage;
             bool ok = true;
@@ -306,7 +304,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
         XRing stage, buf, acc;
         uint32_t ophase = 0;
         bool ok = true;
-        zero_dead_rows<MODE>(a, warp, 4 * C::kGroups, lane);
+        zero_dead_rows<MODE>(a, cta, warp, 4 * C::kGroups, lane);
         __syncwarp();
         while (ok && iter.next(it)) {
             const int r = it.r0 + row;
@@ -493,28 +491,61 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_r0, const __grid_constant
     if (tid == 0 && abort_flag) atomicCAS(a.status, 0, (int)KATA_ERR_TIMEOUT);
 }
 
+constexpr int x_groups(int mode) { return mode == kCrossDkv ? 4 : 2; }
+
+template <int MODE, bool SPLIT>
+__global__ void __launch_bounds__(XCfg<MODE, x_groups(MODE)>::kThreads, 1)
+cross_tc_kernel(const __grid_constant__ XLaunch x) {
+    cross_tc<MODE, x_groups(MODE), SPLIT>(x.maps[0], x.maps[1], x.maps[2], x.maps[3], x.a, blockIdx.x);
+}
+
+// dq and dkv side by side, the SMs shared out by their work: for problems so small
+// that a launch's start and end count (two sequences of 8 query heads on 2 key
+// heads, 1021 queries, 1999 keys, d = 32: 19 and 25 us and a join each, or 37 us and one
+// join).
+__global__ void __launch_bounds__(XCfg<kCrossDkv, 4>::kThreads, 1)
+cross_tc_both(const __grid_constant__ XLaunch q, const __grid_constant__ XLaunch kv) {
+    if ((int)blockIdx.x < kv.a.sched.grid)
+        cross_tc<kCrossDkv, 4, false>(kv.maps[0], kv.maps[1], kv.maps[2], kv.maps[3], kv.a, blockIdx.x);
+    else
+        cross_tc<kCrossDq, 4, false>(q.maps[0], q.maps[1], q.maps[2], q.maps[3], q.a,
+                                     blockIdx.x - kv.a.sched.grid);
+}
+
 template <int MODE, bool SPLIT>
 cudaError_t launch_mode(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    using C = XCfg<MODE, x_groups(MODE)>;
     XLaunch x;
     cudaError_t e = x_launch(static_cast<CrossMode>(MODE), p, io, x);
     if (e != cudaSuccess) return e;
-    if ((e = smem_opt_in_once<cross_tc_kernel<MODE, SPLIT>>(XCfg<MODE>::kSmem)) != cudaSuccess) return e;
+    if ((e = smem_opt_in_once<cross_tc_kernel<MODE, SPLIT>>(C::kSmem)) != cudaSuccess) return e;
     ProfScope prof(MODE == kCrossFwd ? "cross_fwd" : MODE == kCrossDq ? "cross_dq" : "cross_dkv", st);
     if (MODE == kCrossFwd) {  // the call's first kernel
-        cross_tc_kernel<MODE, SPLIT><<<x.a.sched.grid, XCfg<MODE>::kThreads, XCfg<MODE>::kSmem, st>>>(
-            x.maps[0], x.maps[1], x.maps[2], x.maps[3], x.a);
+        cross_tc_kernel<MODE, SPLIT><<<x.a.sched.grid, C::kThreads, C::kSmem, st>>>(x);
         return cudaGetLastError();
     }
-    return launch_dependent(cross_tc_kernel<MODE, SPLIT>, dim3(x.a.sched.grid), (unsigned)XCfg<MODE>::kThreads,
-                            XCfg<MODE>::kSmem, st, x.maps[0], x.maps[1], x.maps[2], x.maps[3], x.a);
+    return launch_dependent(cross_tc_kernel<MODE, SPLIT>, dim3(x.a.sched.grid), (unsigned)C::kThreads, C::kSmem, st, x);
 }
 
 }  // namespace
 
-cudaError_t launch_cross_tc(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
-    if (mode == kCrossDq) return launch_mode<kCrossDq, false>(p, io, st);
-    if (mode == kCrossDkv) return launch_mode<kCrossDkv, false>(p, io, st);
+cudaError_t launch_cross_tc_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     return io.y && p.d <= 32 ? launch_mode<kCrossFwd, true>(p, io, st) : launch_mode<kCrossFwd, false>(p, io, st);
+}
+cudaError_t launch_cross_tc_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    if (!p.together) {
+        const cudaError_t e = launch_mode<kCrossDq, false>(p, io, st);
+        return e != cudaSuccess ? e : launch_mode<kCrossDkv, false>(p, io, st);
+    }
+    using C = XCfg<kCrossDkv, 4>;
+    XLaunch q, kv;
+    cudaError_t e = x_launch(kCrossDq, p, io, q);
+    if (e == cudaSuccess) e = x_launch(kCrossDkv, p, io, kv);
+    if (e == cudaSuccess) e = smem_opt_in_once<cross_tc_both>(C::kSmem);
+    if (e != cudaSuccess) return e;
+    ProfScope prof("cross_bwd", st);
+    return launch_dependent(cross_tc_both, dim3(q.a.sched.grid + kv.a.sched.grid), (unsigned)C::kThreads, C::kSmem, st,
+                            q, kv);
 }
 
 }  // namespace kata

@@ -77,14 +77,14 @@ __device__ __forceinline__ void store_part(float *dst, const uint32_t *o, int d)
 }
 
 // Rows without a visible key, which no unit covers: zeros.  Tile by tile over the
-// grid, by the n_warps warps that call it.
+// mode's CTAs, by the n_warps warps of each that call it.
 template <int MODE>
-__device__ void zero_dead_rows(const XArgs &a, int warp, int n_warps, int lane) {
+__device__ void zero_dead_rows(const XArgs &a, int cta, int warp, int n_warps, int lane) {
     const XSched &sc = a.sched;
     if (!sc.key_lengths) return;
     const int tiles = (sc.rows + kXTile - 1) / kXTile;
     const long long n = a.BH * tiles;
-    for (long long x = (long long)blockIdx.x * n_warps + warp; x < n; x += (long long)gridDim.x * n_warps) {
+    for (long long x = (long long)cta * n_warps + warp; x < n; x += (long long)sc.grid * n_warps) {
         const int bh = (int)(x / tiles), r0 = (int)(x % tiles) * kXTile;
         const int live = cross_length(sc.key_lengths, bh / sc.Hkv, sc.Tk);
         if (MODE == kCrossDkv ? r0 < live : live > 0) continue;
@@ -106,8 +106,8 @@ __device__ void zero_dead_rows(const XArgs &a, int warp, int n_warps, int lane) 
 
 // Arguments and tensor maps (row operands r0, r1, column operands c0, c1) of a mode.
 struct XLaunch {
-    XArgs a;
     CUtensorMap maps[4];
+    XArgs a;
 };
 inline cudaError_t x_launch(CrossMode mode, const CrossPlan &p, const CrossIo &io, XLaunch &x) {
     char *ws = static_cast<char *>(io.ws);

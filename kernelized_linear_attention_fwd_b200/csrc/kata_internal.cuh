@@ -253,6 +253,7 @@ struct CrossPlan {
     bool few;          // forward by launch_cross_few
     int splits[3];     // fp32, per CrossMode: pieces of the summed axis (1: no join)
     XSched sched[3];   // bf16, per CrossMode, and few
+    bool together;     // bf16: dq and dkv in one launch
     // workspace (bytes)
     size_t ws_part[3];  // partial sums of each mode
     size_t ws_part_l;   // forward: partial denominators
@@ -278,7 +279,8 @@ constexpr int kFewRows = 4;
 // CTAs per SM of that kernel for this many rows (64, 80, 128 registers a thread).
 __host__ __device__ constexpr int few_per_sm(int rows) { return rows == 1 ? 4 : rows == 2 ? 3 : 2; }
 cudaError_t launch_cross_few(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
-cudaError_t launch_cross_tc(CrossMode mode, const CrossPlan &p, const CrossIo &io, cudaStream_t st);
+cudaError_t launch_cross_tc_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
+cudaError_t launch_cross_tc_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);  // dq and dkv
 cudaError_t launch_cross_f32_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 cudaError_t launch_cross_f32_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);  // dq and dkv
 // Rows of a CTA and columns of a block of the fp32 kernels.

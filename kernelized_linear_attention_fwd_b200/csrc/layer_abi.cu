@@ -172,7 +172,7 @@ int cross_splits(long long items, long long blocks) {
 // - whole = 1: equal lengths and whole items, dealt evenly, that leave the busiest SM at
 //   most 3% above the average.  (Lengths that differ put stretches of whole items up
 //   to an item apart.)
-bool cross_sched(const CrossPlan &p, CrossMode m, int rows, int cols, XSched &s) {
+bool cross_sched(const CrossPlan &p, CrossMode m, int rows, int cols, int sms, XSched &s) {
     const long long tiles = (rows + kXTile - 1) / kXTile, blocks = (cols + kXCols - 1) / kXCols;
     const long long items = p.BH * tiles;
     if (items >= (1LL << 31) || items > (1LL << 62) / blocks) return false;
@@ -184,7 +184,7 @@ bool cross_sched(const CrossPlan &p, CrossMode m, int rows, int cols, XSched &s)
     s.Tk = p.Tk;
     s.key_lengths = nullptr;
     // CTAs that run at a time, and the fewest units worth one
-    const int full = m == kCrossFwd && p.few ? few_per_sm(p.R) * kPlanSms : kPlanSms, least = m == kCrossFwd && p.few ? 2 : 4;
+    const int full = m == kCrossFwd && p.few ? few_per_sm(p.R) * kPlanSms : sms, least = m == kCrossFwd && p.few ? 2 : 4;
     const long long rounds = (items + full - 1) / full;
     const bool tiny = items < full && blocks <= least;
     s.whole = tiny || items >= 16 * full ? 2 : rounds * full * 100 <= items * 103 ? 1 : 0;
@@ -218,12 +218,18 @@ kata_status cross_plan(int B, int H, int Hkv, int Tq, int Tk, int d, kata_dtype 
     p.ws_rden = stat;
     size_t off = 2 * stat;
     p.few = p.R <= kFewRows;
+    // dq and dkv in one launch while each would take an SM less than some 32 steps; the
+    // SMs go by the steps' times, about 1 : 1.4
+    const long long rt = (p.R + kXTile - 1) / kXTile, kt = (Tk + kXTile - 1) / kXTile;
+    p.together = dtype == KATA_BF16 && p.BH < kPlanSms * 32 / rt / kt;
+    const int sms_q = kPlanSms * 5 / 12;
     for (const CrossMode m : {kCrossFwd, kCrossDq, kCrossDkv}) {
         const long long n = m == kCrossDkv ? Tk : p.R, c = m == kCrossDkv ? p.R : Tk;
         size_t part_rows = 0;  // rows of partial sums
         const bool cut = dtype == KATA_BF16 || (m == kCrossFwd && p.few);
         if (cut) {
-            if (!cross_sched(p, m, (int)n, (int)c, p.sched[m])) return KATA_ERR_UNSUPPORTED;
+            const int sms = !p.together || m == kCrossFwd ? kPlanSms : m == kCrossDq ? sms_q : kPlanSms - sms_q;
+            if (!cross_sched(p, m, (int)n, (int)c, sms, p.sched[m])) return KATA_ERR_UNSUPPORTED;
             part_rows = p.sched[m].whole == 2 ? 0 : (size_t)p.sched[m].grid * 2 * p.sched[m].slot_rows;
             p.splits[m] = 1;
         } else {
