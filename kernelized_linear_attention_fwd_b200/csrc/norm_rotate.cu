@@ -175,9 +175,110 @@ __device__ __forceinline__ float dot8(const Pairs &x, const Pairs &y) {
     return f32x2_lo(t) + f32x2_hi(t);
 }
 
+// A lane's gains of one tensor, in the row's run order.
+template <int D, bool INTER>
+__device__ __forceinline__ Pairs gains(const float *w, const Lane<D, INTER> &L) {
+    Pairs p;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        p.a[i] = f32x2_pack(__float_as_uint(w[L.at(2 * i)]), __float_as_uint(w[L.at(2 * i + 1)]));
+        p.b[i] = f32x2_pack(__float_as_uint(w[L.at(4 + 2 * i)]), __float_as_uint(w[L.at(5 + 2 * i)]));
+    }
+    return p;
+}
+
+// The turn of a lane's pairs: cosine (c), sine (s) and its negative (n).
+struct Turn {
+    uint64_t c[2], s[2], n[2];
+};
+__device__ __forceinline__ Turn turn_of(const float2 (&cs)[4]) {
+    Turn t;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        t.c[i] = f32x2_pack(__float_as_uint(cs[2 * i].x), __float_as_uint(cs[2 * i + 1].x));
+        t.s[i] = f32x2_pack(__float_as_uint(cs[2 * i].y), __float_as_uint(cs[2 * i + 1].y));
+        t.n[i] = t.s[i] ^ 0x8000000080000000ull;
+    }
+    return t;
+}
+
+// One row's share of a lane.  Forward: x normed, times the gains and turned, m the
+// turn with the gains folded in: out_a = x_a m.a + x_b m.b, out_b = x_a k.a + x_b k.b.
+template <int D>
+__device__ __forceinline__ Pairs row_forward(const Pairs &x, const Pairs &m, const Pairs &k, float eps) {
+    const uint64_t r2 = both(rsqrtf(fmaf(row_sum<D>(dot8(x, x)), 1.f / D, eps)));
+    Pairs o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        o.a[i] = f32x2_mul(f32x2_fma(x.a[i], m.a[i], f32x2_mul(x.b[i], m.b[i])), r2);
+        o.b[i] = f32x2_mul(f32x2_fma(x.a[i], k.a[i], f32x2_mul(x.b[i], k.b[i])), r2);
+    }
+    return o;
+}
+__device__ __forceinline__ void fold(const Turn &t, const Pairs &w, Pairs &m, Pairs &k) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        m.a[i] = f32x2_mul(t.c[i], w.a[i]);
+        m.b[i] = f32x2_mul(t.n[i], w.b[i]);
+        k.a[i] = f32x2_mul(t.s[i], w.a[i]);
+        k.b[i] = f32x2_mul(t.c[i], w.b[i]);
+    }
+}
+// Backward: the input's gradient from the output's, y; dw gains the row's share.
+template <int D>
+__device__ __forceinline__ Pairs row_backward(Pairs x, const Pairs &y, const Turn &t, const Pairs &w, Pairs &dw,
+                                              float eps) {
+    const uint64_t r2 = both(rsqrtf(fmaf(row_sum<D>(dot8(x, x)), 1.f / D, eps)));
+    Pairs g, o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        // the gradient turned back
+        g.a[i] = f32x2_fma(y.a[i], t.c[i], f32x2_mul(y.b[i], t.s[i]));
+        g.b[i] = f32x2_fma(y.b[i], t.c[i], f32x2_mul(y.a[i], t.n[i]));
+        x.a[i] = f32x2_mul(x.a[i], r2);  // u
+        x.b[i] = f32x2_mul(x.b[i], r2);
+        dw.a[i] = f32x2_fma(g.a[i], x.a[i], dw.a[i]);
+        dw.b[i] = f32x2_fma(g.b[i], x.b[i], dw.b[i]);
+        g.a[i] = f32x2_mul(g.a[i], w.a[i]);
+        g.b[i] = f32x2_mul(g.b[i], w.b[i]);
+    }
+    const uint64_t nm2 = both(row_sum<D>(dot8(g, x)) * (-1.f / D));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        o.a[i] = f32x2_mul(f32x2_fma(nm2, x.a[i], g.a[i]), r2);
+        o.b[i] = f32x2_mul(f32x2_fma(nm2, x.b[i], g.b[i]), r2);
+    }
+    return o;
+}
+
+// The block's sum of dw into its row of `partial`: lanes of one column, then warps,
+// always in this order.
+template <int D, bool INTER>
+__device__ __forceinline__ void store_dw(const Pairs (&dw)[2], const Lane<D, INTER> &L, float *partial) {
+    __shared__ float red[kNormWarps][2][D];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint64_t q = e < 4 ? dw[m].a[(e & 3) / 2] : dw[m].b[(e & 3) / 2];
+            float v = e & 1 ? f32x2_hi(q) : f32x2_lo(q);
+#pragma unroll
+            for (int o = D / 8; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane < D / 8) red[warp][m][L.at(e)] = v;
+        }
+    __syncthreads();
+    if (threadIdx.x < 2 * D) {
+        float v = 0.f;
+#pragma unroll
+        for (int x = 0; x < kNormWarps; ++x) v += (&red[x][0][0])[threadIdx.x];
+        partial[threadIdx.x] = v;
+    }
+}
+
 // Row groups that a warp loads at a time: 2 KB, of the input or of input and gradient.
 __host__ __device__ constexpr int norm_groups(bool backward, int size) { return (backward ? 4 : 8) / size; }
-// Blocks per SM (64 and 80 registers a thread).
+// Blocks per SM (80 and 128 registers a thread).
 __host__ __device__ constexpr int norm_per_sm(bool backward) { return backward ? 2 : 3; }
 
 template <typename T>
@@ -244,74 +345,28 @@ norm_rotate_kernel(const NormArgs<T> a) {
         for (int m = 0; m < 2; ++m) {
             const int H = a.H[m];
             if (H == 0) continue;
-            Pairs w, c, s;  // c in a: cosine; s in a: sine, in b: -sine
-            {
-                const float4 u = *reinterpret_cast<const float4 *>(&cs_buf[warp][L.p0]);
-                const float4 v = *reinterpret_cast<const float4 *>(&cs_buf[warp][L.p0 + 2]);
-                c.a[0] = f32x2_pack(__float_as_uint(u.x), __float_as_uint(u.z));
-                c.a[1] = f32x2_pack(__float_as_uint(v.x), __float_as_uint(v.z));
-                s.a[0] = f32x2_pack(__float_as_uint(u.y), __float_as_uint(u.w));
-                s.a[1] = f32x2_pack(__float_as_uint(v.y), __float_as_uint(v.w));
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    s.b[i] = s.a[i] ^ 0x8000000080000000ull;
-                    w.a[i] = f32x2_pack(__float_as_uint(w_buf[m][L.at(2 * i)]),
-                                        __float_as_uint(w_buf[m][L.at(2 * i + 1)]));
-                    w.b[i] = f32x2_pack(__float_as_uint(w_buf[m][L.at(4 + 2 * i)]),
-                                        __float_as_uint(w_buf[m][L.at(5 + 2 * i)]));
-                }
-            }
-            Pairs ca, cb;  // forward: y_a = x_a ca.a + x_b cb.a, y_b = x_a ca.b + x_b cb.b
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                ca.a[i] = f32x2_mul(c.a[i], w.a[i]);
-                cb.a[i] = f32x2_mul(s.b[i], w.b[i]);
-                ca.b[i] = f32x2_mul(s.a[i], w.a[i]);
-                cb.b[i] = f32x2_mul(c.a[i], w.b[i]);
-            }
+            const float4 u0 = *reinterpret_cast<const float4 *>(&cs_buf[warp][L.p0]);
+            const float4 u1 = *reinterpret_cast<const float4 *>(&cs_buf[warp][L.p0 + 2]);
+            const float2 cs[4] = {{u0.x, u0.y}, {u0.z, u0.w}, {u1.x, u1.y}, {u1.z, u1.w}};
+            const Turn turn = turn_of(cs);
+            const Pairs w = gains(w_buf[m], L);
+            Pairs fm, fk;
+            if (!BWD) fold(turn, w, fm, fk);
             const int h0 = blockIdx.y * (U * kRows) + sub, stride = gridDim.y * (U * kRows);
             const long long sh = a.sh[m] * kRows, yh = (long long)a.T_ * D * kRows;
             const T *px = a.x[m] + b * a.sb[m] + t * a.st[m] + h0 * a.sh[m];
             const long long y0 = (((long long)b * H + h0) * a.T_ + t) * D;
-
-            auto work = [&](const Row &rx, const Row &rg, T *dst, bool on) {
-                Pairs x = rx.get(), o;
-                const float r = rsqrtf(fmaf(row_sum<D>(dot8(x, x)), 1.f / D, a.eps));
-                const uint64_t r2 = both(r);
-                if (!BWD) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        o.a[i] = f32x2_mul(f32x2_fma(x.a[i], ca.a[i], f32x2_mul(x.b[i], cb.a[i])), r2);
-                        o.b[i] = f32x2_mul(f32x2_fma(x.a[i], ca.b[i], f32x2_mul(x.b[i], cb.b[i])), r2);
-                    }
-                } else {
-                    const Pairs y = rg.get();
-                    Pairs g;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        // the gradient turned back
-                        g.a[i] = f32x2_fma(y.a[i], c.a[i], f32x2_mul(y.b[i], s.a[i]));
-                        g.b[i] = f32x2_fma(y.b[i], c.a[i], f32x2_mul(y.a[i], s.b[i]));
-                        x.a[i] = f32x2_mul(x.a[i], r2);  // u
-                        x.b[i] = f32x2_mul(x.b[i], r2);
-                        dw[m].a[i] = f32x2_fma(g.a[i], x.a[i], dw[m].a[i]);
-                        dw[m].b[i] = f32x2_fma(g.b[i], x.b[i], dw[m].b[i]);
-                        g.a[i] = f32x2_mul(g.a[i], w.a[i]);
-                        g.b[i] = f32x2_mul(g.b[i], w.b[i]);
-                    }
-                    const uint64_t nm2 = both(row_sum<D>(dot8(g, x)) * (-1.f / D));
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        o.a[i] = f32x2_mul(f32x2_fma(nm2, x.a[i], g.a[i]), r2);
-                        o.b[i] = f32x2_mul(f32x2_fma(nm2, x.b[i], g.b[i]), r2);
-                    }
-                }
-                if (on) Row::store(dst, L.o0, L.o1, o);
-            };
-
             T *po = BWD ? a.dx[m] + b * a.db[m] + t * a.dt[m] + h0 * a.dh[m] : a.y[m] + y0;
             const long long oh = BWD ? a.dh[m] * kRows : yh;
             const T *pg = BWD ? a.gy[m] + y0 : nullptr;
+            auto work = [&](const Row &rx, const Row &rg, T *dst, bool on) {
+                Pairs o;
+                if constexpr (BWD)
+                    o = row_backward<D>(rx.get(), rg.get(), turn, w, dw[m], a.eps);
+                else
+                    o = row_forward<D>(rx.get(), fm, fk, a.eps);
+                if (on) Row::store(dst, L.o0, L.o1, o);
+            };
             int h = h0;
             for (; h - sub + U * kRows <= H; h += stride) {
                 Row rx[U], rg[BWD ? U : 1];
@@ -345,27 +400,112 @@ norm_rotate_kernel(const NormArgs<T> a) {
         b = nb;
         t = nt;
     }
-    if (BWD) {
-        // the block's sum of dw: lanes of one column, then warps, always in this order
-        __shared__ float red[kNormWarps][2][D];
+    if constexpr (BWD)
+        store_dw(dw, L, a.partial + ((long long)blockIdx.y * gridDim.x + blockIdx.x) * (2 * D));
+}
+
+// The same for few heads: a warp takes G row groups of each tensor at once, which are
+// all heads of a token, or with one group those of several consecutive tokens, 2^hs
+// rows to a token.  All loads are issued together, before the angles (each lane works
+// out its own four), or a token ahead where the registers hold it: the kernel above
+// waits for the angles, the queries and the keys of a token one after the other.
+// Forward / gradient of 60000 tokens, us, above and so: 8 + 8 heads of 64 80 / 104 and
+// 55 / 92, 6 + 3 heads 61 / 100 and 47 / 76, 12 + 12 heads (four groups) 111 / 155 and
+// 84 / 209, 16 + 16 heads 94 / 180 and 100 / 254; 171680 tokens of 2 + 2 heads 113 / 195
+// and 49 / 70.
+template <typename T, int D, bool INTER, bool BWD, int G>
+__global__ void __launch_bounds__(32 * kNormWarps, 2)
+norm_rotate_packed_kernel(const NormArgs<T> a, int hs) {
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+    constexpr bool AHEAD = BWD ? G == 1 : G * sizeof(T) <= 8;
+    using Row = Row8<T, INTER>;
+    __shared__ float w_buf[2][D];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, sub = lane / kLanes;
+    const Lane<D, INTER> L(lane, a.n_rot);
+    double freq[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        freq[j] = L.p0 + j < a.n_rot ? (double)a.inv_freq[L.p0 + j] * 0.15915494309189533577 : 0.0;
+    for (int x = threadIdx.x; x < 2 * D; x += 32 * kNormWarps) {
+        const float *src = x < D ? a.w[0] : a.w[1];
+        (&w_buf[0][0])[x] = src ? src[x % D] : 1.f;
+    }
+    __syncthreads();
+    Pairs dw[2] = {};
+    const int per = kRows >> hs, h = sub & ((1 << hs) - 1);  // tokens of a warp, the lane's head
+    const long long step = (long long)gridDim.x * kNormWarps * per;
+    const int step_b = (int)(step / a.T_), step_t = (int)(step - (long long)step_b * a.T_);
+    long long tok = ((long long)blockIdx.x * kNormWarps + warp) * per;  // the warp's first token
+    const long long mine = tok + (sub >> hs);
+    int b = (int)(mine / a.T_), t = (int)(mine - (long long)b * a.T_);
+    struct Data {
+        Row x[2][G], g[BWD ? 2 : 1][BWD ? G : 1];
+        long long pos;
+    };
+    auto load = [&](int bb, int tt, bool on, Data &d) {
+        d.pos = on && a.n_rot > 0 ? (a.pos ? a.pos[bb * a.pos_stride + tt] : (long long)tt) : 0;
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint64_t q = e < 4 ? dw[m].a[(e & 3) / 2] : dw[m].b[(e & 3) / 2];
-                float v = e & 1 ? f32x2_hi(q) : f32x2_lo(q);
-#pragma unroll
-                for (int o = kLanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (sub == 0) red[warp][m][L.at(e)] = v;
+            for (int u = 0; u < G; ++u) {
+                const int hu = h + u * kRows;
+                d.x[m][u].zero();
+                if (BWD) d.g[m][u].zero();
+                if (on && hu < a.H[m]) {
+                    d.x[m][u].load(a.x[m] + bb * a.sb[m] + tt * a.st[m] + hu * a.sh[m], L.o0, L.o1);
+                    if (BWD)
+                        d.g[m][u].load(a.gy[m] + (((long long)bb * a.H[m] + hu) * a.T_ + tt) * D, L.o0, L.o1);
+                }
             }
-        __syncthreads();
-        if (threadIdx.x < 2 * D) {
-            float v = 0.f;
-#pragma unroll
-            for (int x = 0; x < kNormWarps; ++x) v += (&red[x][0][0])[threadIdx.x];
-            a.partial[((long long)blockIdx.y * gridDim.x + blockIdx.x) * (2 * D) + threadIdx.x] = v;
+    };
+    Data d;
+    if (AHEAD && tok < a.tokens) load(b, t, mine < a.tokens, d);
+    for (; tok < a.tokens; tok += step) {
+        int nb = b + step_b, nt = t + step_t;
+        if (nt >= a.T_) {
+            nt -= a.T_;
+            ++nb;
         }
+        const long long at = tok + (sub >> hs);
+        Data n;
+        if (AHEAD)
+            load(nb, nt, at + step < a.tokens, n);
+        else
+            load(b, t, at < a.tokens, d);
+        float2 cs[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const double turns = (double)d.pos * freq[j];
+            sincospif((float)(2.0 * (turns - rint(turns))), &cs[j].y, &cs[j].x);
+        }
+        const Turn turn = turn_of(cs);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            if (a.H[m] == 0) continue;
+            const Pairs w = gains(w_buf[m], L);
+            Pairs fm, fk;
+            if (!BWD) fold(turn, w, fm, fk);
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+                if (u > 0 && u * kRows >= a.H[m]) break;
+                const int hu = h + u * kRows;
+                Pairs o;
+                if constexpr (BWD)
+                    o = row_backward<D>(d.x[m][u].get(), d.g[m][u].get(), turn, w, dw[m], a.eps);
+                else
+                    o = row_forward<D>(d.x[m][u].get(), fm, fk, a.eps);
+                if (at < a.tokens && hu < a.H[m]) {
+                    T *po = BWD ? a.dx[m] + b * a.db[m] + t * a.dt[m] + hu * a.dh[m]
+                                : a.y[m] + (((long long)b * a.H[m] + hu) * a.T_ + t) * D;
+                    Row::store(po, L.o0, L.o1, o);
+                }
+            }
+        }
+        if (AHEAD) d = n;
+        b = nb;
+        t = nt;
     }
+    if constexpr (BWD) store_dw(dw, L, a.partial + (long long)blockIdx.x * (2 * D));
 }
 
 // dw = sum of the blocks' partial sums, in a fixed order: a CTA per 16 columns,
@@ -393,8 +533,18 @@ norm_dw_kernel(const float *partial, int n, float *dwq, float *dwk) {
     }
 }
 
-// Blocks of the launch: as many as hold the tokens, at most what the SMs hold at a time;
-// if the tokens fill less than that, the heads are spread over grid.y.
+int max_heads(const NormRotate &p) { return p.H[0] > p.H[1] ? p.H[0] : p.H[1]; }
+
+// log2 of the rows that a token takes in the packed kernel; -1: too many heads for it.
+// The forward takes up to four groups, but four full ones go faster above (the figures
+// are at the kernel), the gradient two, by its registers.
+int norm_packed(const NormRotate &p) {
+    const int hm = max_heads(p), rows = 256 / p.d;
+    int hs = 0;
+    while ((1 << hs) < hm && (1 << hs) < rows) ++hs;
+    return hm <= (p.backward ? 2 * rows : 4 * rows - 1) ? hs : -1;
+}
+
 template <typename T, int D, bool INTER, bool BWD>
 cudaError_t launch_one(const NormRotate &p, cudaStream_t st) {
     NormArgs<T> a;
@@ -423,7 +573,16 @@ cudaError_t launch_one(const NormRotate &p, cudaStream_t st) {
     const dim3 grid = norm_rotate_grid(p);
     {
         ProfScope prof(BWD ? "norm_rotate_bwd" : "norm_rotate", st);
-        norm_rotate_kernel<T, D, INTER, BWD><<<grid, 32 * kNormWarps, 0, st>>>(a);
+        const int hs = norm_packed(p);
+        const int groups = (max_heads(p) + 256 / D - 1) / (256 / D);
+        if (hs >= 0 && groups == 1)
+            norm_rotate_packed_kernel<T, D, INTER, BWD, 1><<<grid, 32 * kNormWarps, 0, st>>>(a, hs);
+        else if (hs >= 0 && (BWD || groups == 2))
+            norm_rotate_packed_kernel<T, D, INTER, BWD, 2><<<grid, 32 * kNormWarps, 0, st>>>(a, hs);
+        else if (!BWD && hs >= 0)
+            norm_rotate_packed_kernel<T, D, INTER, false, 4><<<grid, 32 * kNormWarps, 0, st>>>(a, hs);
+        else
+            norm_rotate_kernel<T, D, INTER, BWD><<<grid, 32 * kNormWarps, 0, st>>>(a);
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !BWD || (!p.dw[0] && !p.dw[1])) return e;
@@ -450,19 +609,22 @@ cudaError_t launch_t(const NormRotate &p, cudaStream_t st) {
 
 }  // namespace
 
+// Blocks of the launch: as many as hold the tokens, at most what the SMs hold at a
+// time; if the tokens of the unpacked kernel fill less than that, the heads are spread
+// over grid.y.  The same for both types, as the workspace is.
 dim3 norm_rotate_grid(const NormRotate &p) {
     const long long tokens = (long long)p.B * p.T;
-    const long long blocks = (tokens + kNormWarps - 1) / kNormWarps;
-    const long long full = (long long)norm_per_sm(p.backward) * kPlanSms;
+    const int hs = norm_packed(p);
+    const long long full = (long long)(hs >= 0 ? 2 : norm_per_sm(p.backward)) * kPlanSms;
+    const long long per = kNormWarps * (hs >= 0 ? (256 / p.d) >> hs : 1);  // tokens of a block
+    const long long blocks = (tokens + per - 1) / per;
     const int gx = (int)(blocks < full ? blocks : full);
-    // row groups a warp could leave to others
-    const int rows = norm_groups(p.backward, p.dtype == KATA_BF16 ? 2 : 4) * (256 / p.d);
-    const int hm = p.H[0] > p.H[1] ? p.H[0] : p.H[1];
-    const int groups = (hm + rows - 1) / rows;
+    if (hs >= 0) return dim3(gx);
+    const int rows = norm_groups(p.backward, 2) * (256 / p.d);  // row groups a warp could leave to others
+    const int hm = max_heads(p);
     int gy = (int)(full / gx);
-    if (gy > groups) gy = groups;
-    if (gy < 1) gy = 1;
-    return dim3(gx, gy);
+    if (gy > (hm + rows - 1) / rows) gy = (hm + rows - 1) / rows;
+    return dim3(gx, gy < 1 ? 1 : gy);
 }
 
 cudaError_t launch_norm_rotate(const NormRotate &p, cudaStream_t st) {

@@ -152,6 +152,16 @@ def test_cross_backward_refusals(lib, bad, status):
     assert cross(lib, "b", **bad) == status
 
 
+def test_norm_workspace(lib):
+    W = lib.kata_qk_norm_rotate_backward_workspace_bytes
+    top = 2 ** 31 - 2 ** 17
+    assert W(1, top - 1, 1, 1, 64) > 0 and W(top - 1, 1, 1, 1, 64) > 0
+    assert W(1, top, 1, 1, 64) == 0 and W(top, 1, 1, 1, 64) == 0
+    assert W(1, 2 ** 31 - 1, 1, 1, 64) == 0 and W(2 ** 31 - 1, 1, 1, 1, 64) == 0
+    # a row of partial sums per block, which a single token has few of
+    assert 0 < W(1, 1, 1, 1, 64) <= 2 * 64 * 4 + 255 and W(1, 10 ** 6, 32, 32, 16) <= 4 * 148 * 2 * 16 * 4 + 255
+
+
 def test_cross_workspace(lib):
     W, V = lib.kata_cross_forward_workspace_bytes, lib.kata_cross_backward_workspace_bytes
     for bad, _ in SIZES:

@@ -90,6 +90,16 @@ def test_shapes(B, T, H, Hk, dtype):
     check(B, T, H, Hk, 64, dtype, 32, False, seed=B + T)
 
 
+@pytest.mark.parametrize("d,H,Hk", [(64, 2, 1), (64, 3, 2), (64, 4, 0), (64, 4, 8), (64, 9, 2), (64, 15, 15), (64, 5, 16),
+                                    (32, 1, 2), (32, 7, 3), (32, 16, 9), (32, 31, 4), (16, 1, 1), (16, 9, 2), (16, 17, 3),
+                                    (16, 63, 1)])
+@pytest.mark.parametrize("dtype,inter", [("bf16", True), ("f32", False)])
+def test_head_counts_about_a_warps_rows(d, H, Hk, dtype, inter):
+    # tokens that end inside a warp's, batches that end inside them, several turns of a warp
+    check(3, 67, H, Hk, d, dtype, d // 2, inter, seed=H + Hk)
+    check(1, 2371 * 64 // d + 1, H, Hk, d, dtype, d // 4, inter, seed=H + Hk + 1)
+
+
 def test_no_gain_and_default_positions():
     check(2, 70, 3, 2, 32, "f32", 16, False, seed=5, pos=None, weights=False)
 
