@@ -22,7 +22,7 @@
 // depend on order.
 //
 // Roundings to bf16: the weights (and ds) that go back into the tensor cores as
-// operands, once each.  The denominator is the product of the same rounded weights
+// operands, once each (or twice, SPLIT below).  The denominator is the product of the same rounded weights
 // with a column of ones, in 16 columns more of the product with the values (which
 // the 128-row operand's read pays for anyway), so that y is a convex combination of
 // values to fp32: with one visible key y = v and, D being formed from the same y,
@@ -41,8 +41,9 @@
 //   0 .. 127       accumulators: forward: O and l; dq: two of 64 columns, items in
 //                  turn; dkv: dV and dK
 //   128, 256       S of successive steps (forward: and 384); the weights replace it:
-//                  per 16 scores 8 columns of w (SPLIT: and 8 of low parts), of ds, or
-//                  of w / l and 8 of ds
+//                  per 16 scores 8 columns of w or ds (SPLIT: and 8 of low parts), or 8 of
+//                  w / l and 8 of ds (SPLIT: their low parts 128 columns on, in the second
+//                  region, which there is none of then)
 //   384            dq, dkv: P, free again once the warps have read it
 //
 // so the next step's S is formed while this step's scores are turned, its P right
@@ -60,7 +61,7 @@ namespace kata {
 namespace {
 
 // GROUPS: of 4 warps that turn scores into weights; the other warps come behind them.
-template <int MODE, int GROUPS>
+template <int MODE, int GROUPS, bool SPLIT>
 struct XCfg {
     static constexpr bool kFwd = MODE == kCrossFwd, kDkv = MODE == kCrossDkv;
     static constexpr int kGroups = GROUPS;
@@ -76,9 +77,16 @@ struct XCfg {
     static constexpr int kOnes = kFwd ? 16384 : 0;  // a 128 x 64 operand of ones
     static constexpr int kSmem = 2 * kSlot + kStages * (kStage + kStat) + kOnes + 1024;
     // tensor memory: accumulators in columns 0 .. 127, regions of S, the one of P
-    static constexpr int kRegions = kFwd ? 3 : 2;
+    static constexpr int kRegions = kFwd ? 3 : kDkv && SPLIT ? 1 : 2;
+    static constexpr uint32_t kLow = kDkv ? 128 : 8;  // SPLIT: from a part to its low part
     static constexpr uint32_t kColS = 128, kColP = 384;
 };
+
+// What two numbers lose by their rounding to bf16, as bf16.
+__device__ __forceinline__ uint32_t low_part(uint64_t x, uint32_t rounded) {
+    return f32x2_to_bf16x2(
+        f32x2_add(x, f32x2_pack(rounded << 16, rounded & 0xFFFF0000u) ^ 0x8000000080000000ull));
+}
 
 template <typename C>
 struct XBars {
@@ -89,17 +97,24 @@ struct XBars {
     uint64_t ofull[2], ofree[2], drain[4];
 };
 
-// SPLIT: the weights as two bf16 numbers each (high and low part), which takes twice
-// the products that accumulate: the forward of a training step with d <= 32.  Its y
-// gives the backward pass D = dy.y, and an error of D enters every key's gradient
-// with one sign: next to the other roundings it is as 1 / sqrt(d).  Error of dq
-// relative to exact, rms, without and with (0.00166 of it the output's rounding):
-// d = 16 0.0026, 0.0025; d = 32 0.0025, 0.0024; d = 64 0.0024, 0.0024.  For d = 64 it
-// would take the forward of 2048 queries on 4096 keys half as long again.
+// SPLIT: what goes back into the products (w, ds, w / l) as two bf16 numbers each, a
+// high and a low part, which takes twice the products that accumulate.  Used by
+// training steps (CrossPlan::split) where the rounding of one number would show:
+//
+// - The forward, d <= 32: its y gives the backward pass D = dy.y, and an error of D
+//   enters every key's gradient with one sign: next to the other roundings it is as
+//   1 / sqrt(d).  Also with up to 256 keys, whose roundings do not average out.
+//   For d = 64 and many keys it would take half as long again (2048 queries on 4096 keys)
+//   for an error of dq of 0.0024 either way.
+// - dq, d = 16: dq is orthogonal to q, as y does not depend on q's length, while the
+//   errors of ds lie mostly along q: 0.0025 of dq, rms (0.00166 of it the output's
+//   rounding), without, 0.0017 with it.
+// - dq and dkv with up to 32 rows or 32 keys: few roundings enter a sum, and with two
+//   keys, say, p and D cancel (1.6 to 2.4 times the output's own rounding without).
 template <int MODE, int GROUPS, bool SPLIT>
 __device__ __forceinline__ void cross_tc(const CUtensorMap &tm_r0, const CUtensorMap &tm_r1, const CUtensorMap &tm_c0,
                                          const CUtensorMap &tm_c1, const XArgs &a, int cta) {
-    using C = XCfg<MODE, GROUPS>;
+    using C = XCfg<MODE, GROUPS, SPLIT>;
     constexpr bool kFwd = C::kFwd, kDkv = C::kDkv;
     extern __shared__ uint8_t smem_raw[];
     __shared__ XBars<C> bars;
@@ -280,7 +295,7 @@ __device__ __forceinline__ void cross_tc(const CUtensorMap &tm_r0, const CUtenso
                     if (SPLIT) {
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            mma_ts(tm + 64 * o, w + 16 * ks + 8, desc_at(c, 2048 * ks), id, 1);
+                            mma_ts(tm + 64 * o, w + 16 * ks + C::kLow, desc_at(c, 2048 * ks), id, 1);
                     }
                     mma_commit(&bars.sfree[buf.i]);
                     buf.next(C::kRegions);
@@ -342,12 +357,10 @@ __device__ __forceinline__ void cross_tc(const CUtensorMap &tm_r0, const CUtenso
                                 const uint64_t s2 = f32x2_pack(v[16 * h + 2 * y], v[16 * h + 2 * y + 1]);
                                 const uint64_t w2 = f32x2_mul(s2, s2);
                                 w[y] = f32x2_to_bf16x2(w2);
-                                if (SPLIT)
-                                    e[y] = f32x2_to_bf16x2(f32x2_add(
-                                        w2, f32x2_pack(w[y] << 16, w[y] & 0xFFFF0000u) ^ 0x8000000080000000ull));
+                                if (SPLIT) e[y] = low_part(w2, w[y]);
                             }
                             tmem_st8(tS + 32 * g + 16 * h, w);
-                            if (SPLIT) tmem_st8(tS + 32 * g + 16 * h + 8, e);
+                            if (SPLIT) tmem_st8(tS + 32 * g + 16 * h + C::kLow, e);
                         }
                     }
                 } else if constexpr (kDkv) {
@@ -378,7 +391,7 @@ __device__ __forceinline__ void cross_tc(const CUtensorMap &tm_r0, const CUtenso
                         tmem_ld_wait();
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {  // 16 columns: 8 of w / l, 8 of ds / 2
-                            uint32_t w[4], e[4];
+                            uint32_t w[4], e[4], wl[4], el[4];
 #pragma unroll
                             for (int y = 0; y < 4; ++y) {
                                 const int j = 2 * h + y / 2, c = 8 * h + 2 * y;
@@ -387,8 +400,17 @@ __device__ __forceinline__ void cross_tc(const CUtensorMap &tm_r0, const CUtenso
                                 const uint64_t d2 = f32x2_pack(__float_as_uint(fd[j].x), __float_as_uint(fd[j].y));
                                 const uint64_t r2 = f32x2_pack(__float_as_uint(fr[j].x), __float_as_uint(fr[j].y));
                                 const uint64_t sr2 = f32x2_mul(s2, r2);
-                                w[y] = f32x2_to_bf16x2(f32x2_mul(s2, sr2));
-                                e[y] = f32x2_to_bf16x2(f32x2_mul(sr2, f32x2_add(g2, d2)));
+                                const uint64_t w2 = f32x2_mul(s2, sr2), e2 = f32x2_mul(sr2, f32x2_add(g2, d2));
+                                w[y] = f32x2_to_bf16x2(w2);
+                                e[y] = f32x2_to_bf16x2(e2);
+                                if (SPLIT) {
+                                    wl[y] = low_part(w2, w[y]);
+                                    el[y] = low_part(e2, e[y]);
+                                }
+                            }
+                            if (SPLIT) {
+                                tmem_st_16x128b_x2(tSu + 16 * h + C::kLow, wl);
+                                tmem_st_16x128b_x2(tSu + 16 * h + 8 + C::kLow, el);
                             }
                             tmem_st_16x128b_x2(tSu + 16 * h, w);
                             tmem_st_16x128b_x2(tSu + 16 * h + 8, e);
@@ -397,7 +419,7 @@ __device__ __forceinline__ void cross_tc(const CUtensorMap &tm_r0, const CUtenso
                 } else {
 #pragma unroll
                     for (int h = 0; h < C::kCols / 16; ++h) {
-                        uint32_t v[16], g[16], w[8];
+                        uint32_t v[16], g[16], w[8], e[8];
                         tmem_ld16(tP + 16 * h, g);
                         tmem_ld16(tS + 16 * h, v);
                         tmem_ld_wait();
@@ -414,10 +436,14 @@ __device__ __forceinline__ void cross_tc(const CUtensorMap &tm_r0, const CUtenso
                             }
                         }
 #pragma unroll
-                        for (int y = 0; y < 8; ++y)
-                            w[y] = f32x2_to_bf16x2(f32x2_mul(f32x2_pack(v[2 * y], v[2 * y + 1]),
-                                                             f32x2_add(f32x2_pack(g[2 * y], g[2 * y + 1]), nd)));
+                        for (int y = 0; y < 8; ++y) {
+                            const uint64_t e2 = f32x2_mul(f32x2_pack(v[2 * y], v[2 * y + 1]),
+                                                          f32x2_add(f32x2_pack(g[2 * y], g[2 * y + 1]), nd));
+                            w[y] = f32x2_to_bf16x2(e2);
+                            if (SPLIT) e[y] = low_part(e2, w[y]);
+                        }
                         tmem_st8(tS + 16 * h, w);
+                        if (SPLIT) tmem_st8(tS + 16 * h + C::kLow, e);
                     }
                 }
                 // keys (forward: values) past the visible ones may be anything (NaN times a zero
@@ -494,7 +520,7 @@ __device__ __forceinline__ void cross_tc(const CUtensorMap &tm_r0, const CUtenso
 constexpr int x_groups(int mode) { return mode == kCrossDkv ? 4 : 2; }
 
 template <int MODE, bool SPLIT>
-__global__ void __launch_bounds__(XCfg<MODE, x_groups(MODE)>::kThreads, 1)
+__global__ void __launch_bounds__(XCfg<MODE, x_groups(MODE), SPLIT>::kThreads, 1)
 cross_tc_kernel(const __grid_constant__ XLaunch x) {
     cross_tc<MODE, x_groups(MODE), SPLIT>(x.maps[0], x.maps[1], x.maps[2], x.maps[3], x.a, blockIdx.x);
 }
@@ -503,18 +529,19 @@ cross_tc_kernel(const __grid_constant__ XLaunch x) {
 // that a launch's start and end count (two sequences of 8 query heads on 2 key
 // heads, 1021 queries, 1999 keys, d = 32: 19 and 25 us and a join each, or 37 us and one
 // join).
-__global__ void __launch_bounds__(XCfg<kCrossDkv, 4>::kThreads, 1)
+template <bool SPLIT_Q, bool SPLIT_KV>
+__global__ void __launch_bounds__(XCfg<kCrossDkv, 4, SPLIT_KV>::kThreads, 1)
 cross_tc_both(const __grid_constant__ XLaunch q, const __grid_constant__ XLaunch kv) {
     if ((int)blockIdx.x < kv.a.sched.grid)
-        cross_tc<kCrossDkv, 4, false>(kv.maps[0], kv.maps[1], kv.maps[2], kv.maps[3], kv.a, blockIdx.x);
+        cross_tc<kCrossDkv, 4, SPLIT_KV>(kv.maps[0], kv.maps[1], kv.maps[2], kv.maps[3], kv.a, blockIdx.x);
     else
-        cross_tc<kCrossDq, 4, false>(q.maps[0], q.maps[1], q.maps[2], q.maps[3], q.a,
+        cross_tc<kCrossDq, 4, SPLIT_Q>(q.maps[0], q.maps[1], q.maps[2], q.maps[3], q.a,
                                      blockIdx.x - kv.a.sched.grid);
 }
 
 template <int MODE, bool SPLIT>
 cudaError_t launch_mode(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
-    using C = XCfg<MODE, x_groups(MODE)>;
+    using C = XCfg<MODE, x_groups(MODE), SPLIT>;
     XLaunch x;
     cudaError_t e = x_launch(static_cast<CrossMode>(MODE), p, io, x);
     if (e != cudaSuccess) return e;
@@ -527,25 +554,31 @@ cudaError_t launch_mode(const CrossPlan &p, const CrossIo &io, cudaStream_t st) 
     return launch_dependent(cross_tc_kernel<MODE, SPLIT>, dim3(x.a.sched.grid), (unsigned)C::kThreads, C::kSmem, st, x);
 }
 
-}  // namespace
-
-cudaError_t launch_cross_tc_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
-    return io.y && p.d <= 32 ? launch_mode<kCrossFwd, true>(p, io, st) : launch_mode<kCrossFwd, false>(p, io, st);
-}
-cudaError_t launch_cross_tc_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+template <bool SPLIT_Q, bool SPLIT_KV>
+cudaError_t launch_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     if (!p.together) {
-        const cudaError_t e = launch_mode<kCrossDq, false>(p, io, st);
-        return e != cudaSuccess ? e : launch_mode<kCrossDkv, false>(p, io, st);
+        const cudaError_t e = launch_mode<kCrossDq, SPLIT_Q>(p, io, st);
+        return e != cudaSuccess ? e : launch_mode<kCrossDkv, SPLIT_KV>(p, io, st);
     }
-    using C = XCfg<kCrossDkv, 4>;
+    using C = XCfg<kCrossDkv, 4, SPLIT_KV>;
     XLaunch q, kv;
     cudaError_t e = x_launch(kCrossDq, p, io, q);
     if (e == cudaSuccess) e = x_launch(kCrossDkv, p, io, kv);
-    if (e == cudaSuccess) e = smem_opt_in_once<cross_tc_both>(C::kSmem);
+    if (e == cudaSuccess) e = smem_opt_in_once<cross_tc_both<SPLIT_Q, SPLIT_KV>>(C::kSmem);
     if (e != cudaSuccess) return e;
     ProfScope prof("cross_bwd", st);
-    return launch_dependent(cross_tc_both, dim3(q.a.sched.grid + kv.a.sched.grid), (unsigned)C::kThreads, C::kSmem, st,
-                            q, kv);
+    return launch_dependent(cross_tc_both<SPLIT_Q, SPLIT_KV>, dim3(q.a.sched.grid + kv.a.sched.grid), (unsigned)C::kThreads,
+                            C::kSmem, st, q, kv);
+}
+
+}  // namespace
+
+cudaError_t launch_cross_tc_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    return io.y && p.split[kCrossFwd] ? launch_mode<kCrossFwd, true>(p, io, st) : launch_mode<kCrossFwd, false>(p, io, st);
+}
+cudaError_t launch_cross_tc_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
+    if (p.split[kCrossDkv]) return launch_backward<true, true>(p, io, st);
+    return p.split[kCrossDq] ? launch_backward<true, false>(p, io, st) : launch_backward<false, false>(p, io, st);
 }
 
 }  // namespace kata

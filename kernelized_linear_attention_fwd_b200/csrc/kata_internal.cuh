@@ -251,6 +251,7 @@ struct CrossPlan {
     int R;             // rows per problem
     int R_pad;         // R rounded up to 128: row stride of the statistics
     bool few;          // forward by launch_cross_few
+    bool split[3];      // bf16, per CrossMode, in training: operands as two bf16 numbers
     int splits[3];     // fp32, per CrossMode: pieces of the summed axis (1: no join)
     XSched sched[3];   // bf16, per CrossMode, and few
     bool together;     // bf16: dq and dkv in one launch

@@ -224,6 +224,14 @@ kata_status cross_plan(int B, int H, int Hkv, int Tq, int Tk, int d, kata_dtype 
     const long long rt = (p.R + kXTile - 1) / kXTile, kt = (Tk + kXTile - 1) / kXTile;
     p.together = dtype == KATA_BF16 && p.BH < kPlanSms * 32 / rt / kt;
     const int sms_q = kPlanSms * 5 / 12;
+    // Where the error of a training step's rounded weights shows (cross_tc.cu): the
+    // forward of heads up to 32 or of few keys (256 keys: 57 us, 66 so, for 3 sequences of
+    // 16 heads and 4000 queries), dq of heads of 16, everything if few rows meet in a
+    // sum (16 rows on 4000 keys, 48 heads: backward 79 us, 89 so).
+    const bool few_terms = p.R <= 32 || Tk <= 32;
+    p.split[kCrossFwd] = d <= 32 || Tk <= 256 || few_terms;
+    p.split[kCrossDq] = d == 16 || few_terms;
+    p.split[kCrossDkv] = few_terms;
     for (const CrossMode m : {kCrossFwd, kCrossDq, kCrossDkv}) {
         const long long n = m == kCrossDkv ? Tk : p.R, c = m == kCrossDkv ? p.R : Tk;
         size_t part_rows = 0;  // rows of partial sums

@@ -126,11 +126,12 @@ def cross_grad(dout, q, k, v, lengths=None):
     return (c @ kk).reshape(q.shape), c.transpose(-1, -2) @ qr, (s * s * inv).transpose(-1, -2) @ g
 
 
-def cross_bounds(q, k, v, dtype, lengths=None, dout=None):
+def cross_bounds(q, k, v, dtype, lengths=None, dout=None, split=False):
     """Elementwise bounds of the kernels' errors, to first order and times 1.1.
 
     e is the relative error of an operand that goes back into the products (bf16:
-    half a step; fp32: none beyond a), a that of a sum relative to the sum of
+    half a step, or with `split`, as two numbers, that of a half step; fp32: none
+    beyond a), a that of a sum relative to the sum of
     its terms' magnitudes: chains of up to 64 terms, then of up to Tk / 64 (fp32) or
     of Tk / 16 (tensor cores, which may truncate: a whole step each).
 
@@ -145,6 +146,7 @@ def cross_bounds(q, k, v, dtype, lengths=None, dout=None):
     qr, kk, vv, _ = _parts(q, k, v, lengths)
     Tk, R = kk.shape[2], qr.shape[2]
     e = HALF[dtype] if dtype == torch.bfloat16 else 0.0
+    e = e * e if split else e
     n = max(Tk, R)
     a = U * (64 + 8 + (n / 64 if dtype == torch.float32 else 2 * n / 16))
     half = HALF[dtype]

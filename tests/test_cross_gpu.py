@@ -211,6 +211,29 @@ def test_gradient_against_differences():
         assert abs(num - ana) <= tol + 1e-7 * scale
 
 
+@pytest.mark.parametrize("d", [16, 32, 64])
+@pytest.mark.parametrize("H,Hk,Tq,Tk", [(2, 2, 300, 1), (2, 1, 1, 2), (4, 2, 16, 5), (3, 3, 700, 9), (8, 8, 130, 32),
+                                        (2, 2, 32, 1000), (4, 1, 8, 300), (1, 1, 1, 4097), (6, 3, 5, 130)])
+def test_few_terms_keep_their_precision(H, Hk, Tq, Tk, d):
+    # the operands go back as two bf16 numbers: only the outputs' rounding is left
+    q, k, v, g = make(2, H, Hk, Tq, Tk, d, "bf16", Tq + Tk)
+    n = lens(Tk, max(1, Tk // 2))
+    y, den = forward(q, k, v, n)[1:]
+    got = K.kata_cross_backward(g, q, k, v, y, den, key_lengths=n)
+    for a, r, b in zip(got, O.cross_grad(g, q, k, v, n), O.cross_bounds(q, k, v, q.dtype, n, dout=g, split=True)):
+        assert O.worst(a, r, b) <= 1
+
+
+@pytest.mark.parametrize("Tq,Tk", [(257, 700), (40, 4000), (1000, 33)])
+def test_query_gradient_of_the_smallest_heads_keeps_its_precision(Tq, Tk):
+    q, k, v, g = make(2, 4, 2, Tq, Tk, 16, "bf16", Tq)
+    n = lens(Tk, Tk // 3)
+    y, den = forward(q, k, v, n)[1:]
+    dq = K.kata_cross_backward(g, q, k, v, y, den, key_lengths=n)[0]
+    bound = O.cross_bounds(q, k, v, q.dtype, n, dout=g, split=True)[0]
+    assert O.worst(dq, O.cross_grad(g, q, k, v, n)[0], bound) <= 1
+
+
 def test_outputs_are_convex_combinations():
     q, k, v, _ = make(1, 2, 2, 100, 400, 64, "bf16", seed=14)
     _, y, _ = forward(q, k, v, None)
