@@ -58,6 +58,10 @@ struct Row8<__nv_bfloat16, INTER> {
         v[1] = __ldg(reinterpret_cast<const uint2 *>(row + o1));
     }
     __device__ __forceinline__ void zero() { v[0] = v[1] = make_uint2(0u, 0u); }
+    __device__ __forceinline__ void load_shared(uint32_t at0, uint32_t at1) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0].x), "=r"(v[0].y) : "r"(at0));
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[1].x), "=r"(v[1].y) : "r"(at1));
+    }
     __device__ __forceinline__ Pairs get() const {
         Pairs p;
         if (INTER) {
@@ -96,6 +100,12 @@ struct Row8<float, INTER> {
         v[1] = __ldg(reinterpret_cast<const uint4 *>(row + o1));
     }
     __device__ __forceinline__ void zero() { v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void load_shared(uint32_t at0, uint32_t at1) {
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w) : "r"(at0));
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[1].x), "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w) : "r"(at1));
+    }
     __device__ __forceinline__ Pairs get() const {
         Pairs p;
         if (INTER) {
@@ -224,29 +234,31 @@ __device__ __forceinline__ void fold(const Turn &t, const Pairs &w, Pairs &m, Pa
         k.b[i] = f32x2_mul(t.c[i], w.b[i]);
     }
 }
-// Backward: the input's gradient from the output's, y; dw gains the row's share.
+// Backward: the input's gradient from the output's, y; dw gains the row's share.  With
+// t = r g: dw += t x, dx = w t - x r^2 mean(w t x).
 template <int D>
-__device__ __forceinline__ Pairs row_backward(Pairs x, const Pairs &y, const Turn &t, const Pairs &w, Pairs &dw,
+__device__ __forceinline__ Pairs row_backward(const Pairs &x, const Pairs &y, const Turn &t, const Pairs &w, Pairs &dw,
                                               float eps) {
-    const uint64_t r2 = both(rsqrtf(fmaf(row_sum<D>(dot8(x, x)), 1.f / D, eps)));
+    const float r = rsqrtf(fmaf(row_sum<D>(dot8(x, x)), 1.f / D, eps));
+    const uint64_t r2 = both(r);
     Pairs g, o;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         // the gradient turned back
         g.a[i] = f32x2_fma(y.a[i], t.c[i], f32x2_mul(y.b[i], t.s[i]));
         g.b[i] = f32x2_fma(y.b[i], t.c[i], f32x2_mul(y.a[i], t.n[i]));
-        x.a[i] = f32x2_mul(x.a[i], r2);  // u
-        x.b[i] = f32x2_mul(x.b[i], r2);
+        g.a[i] = f32x2_mul(g.a[i], r2);
+        g.b[i] = f32x2_mul(g.b[i], r2);
         dw.a[i] = f32x2_fma(g.a[i], x.a[i], dw.a[i]);
         dw.b[i] = f32x2_fma(g.b[i], x.b[i], dw.b[i]);
         g.a[i] = f32x2_mul(g.a[i], w.a[i]);
         g.b[i] = f32x2_mul(g.b[i], w.b[i]);
     }
-    const uint64_t nm2 = both(row_sum<D>(dot8(g, x)) * (-1.f / D));
+    const uint64_t c = both(row_sum<D>(dot8(g, x)) * (r * (-1.f / D)) * r);  // no r^2: it may overflow
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        o.a[i] = f32x2_mul(f32x2_fma(nm2, x.a[i], g.a[i]), r2);
-        o.b[i] = f32x2_mul(f32x2_fma(nm2, x.b[i], g.b[i]), r2);
+        o.a[i] = f32x2_fma(c, x.a[i], g.a[i]);
+        o.b[i] = f32x2_fma(c, x.b[i], g.b[i]);
     }
     return o;
 }
@@ -276,7 +288,8 @@ __device__ __forceinline__ void store_dw(const Pairs (&dw)[2], const Lane<D, INT
     }
 }
 
-// Row groups that a warp loads at a time: 2 KB, of the input or of input and gradient.
+// Row groups of a set, which a warp loads at a time: 2 KB, of the input or of input and
+// gradient.
 __host__ __device__ constexpr int norm_groups(bool backward, int size) { return (backward ? 4 : 8) / size; }
 // Blocks per SM (80 and 128 registers a thread).
 __host__ __device__ constexpr int norm_per_sm(bool backward) { return backward ? 2 : 3; }
@@ -301,13 +314,35 @@ struct NormArgs {
     float eps;
 };
 
-// A warp loads up to U row groups at a time; what is left of a token's heads goes
-// group by group.  The arithmetic is packed (fp32 pairs) and the forward's gains are
-// folded into the angles once per token and tensor: 139 us without either for 65536
-// tokens of 16 + 16 heads of 64 (537 MB), 95 us so, 5.7 TB/s.  The gradient (32768
-// tokens of 16 + 4 heads, 252 MB) takes 70 us, 3.6 TB/s: half of its warps' time is
-// waiting for loads, and neither more warps of fewer registers, nor more rows at a
-// time, nor loading a set of rows ahead across tokens changed it (70 to 76 us).
+// cp.async of N bytes; zeros if not `on` (the address is then not read).
+template <int N>
+__device__ __forceinline__ void async_copy(uint32_t dst, const void *src, bool on) {
+    const int n = on ? N : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void async_copy(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+constexpr int kSetBytes = 2048, kNormStages = 3;
+constexpr int kNormRing = kNormWarps * kNormStages * kSetBytes;
+
+// A warp walks its tokens' sets of U row groups and loads two sets ahead, across
+// tensors and tokens, into a ring in shared memory of which every lane reads what it
+// copied itself (so nothing but its own copies is waited for); the gradient with sets of
+// twice the rows and the ring of four sets: no faster.  Loads into registers, one set at
+// a time, took 95 us for 65536 tokens of 16 + 16 heads of 64 (537 MB; so 87 us, 6.2 TB/s), and
+// 72 us for the gradient of 32768 tokens of 16 + 4 heads (252 MB; so 61 us, 4.1 TB/s: its
+// arithmetic keeps two thirds of the issue slots busy).  The arithmetic is packed (fp32
+// pairs) and the forward's gains are folded into the angles once per token and tensor
+// (139 us without either).
+
 template <typename T, int D, bool INTER, bool BWD>
 __global__ void __launch_bounds__(32 * kNormWarps, norm_per_sm(BWD))
 norm_rotate_kernel(const NormArgs<T> a) {
@@ -325,26 +360,109 @@ norm_rotate_kernel(const NormArgs<T> a) {
     __syncthreads();
     Pairs dw[2] = {};
 
-    // this warp's tokens, every n_warps-th, as (b, t)
+    extern __shared__ __align__(16) uint8_t ring[];
+    constexpr int V = 4 * sizeof(T), X = BWD ? 2 : 1;  // bytes of a run; tensors read
+    static_assert(U * X * 2 * V * 32 == kSetBytes, "size of a set");
+    // a stage: group by group two runs of x, then of the gradient, each 32 lanes side by side
+    const uint32_t ring_at = smem_u32(ring) + warp * (kNormStages * kSetBytes) + lane * V;
+
+    // this warp's tokens, every n_warps-th, as (b, t); a token's sets: U groups of its
+    // queries, every gridDim.y-th, then of its keys
     const int n_warps = gridDim.x * kNormWarps, tok0 = blockIdx.x * kNormWarps + warp;
     const int step_b = n_warps / a.T_, step_t = n_warps - step_b * a.T_;
     int b = tok0 / a.T_, t = tok0 - b * a.T_;
     int left = tok0 < a.tokens ? (int)((a.tokens - tok0 + n_warps - 1) / n_warps) : 0;
+    int n_sets[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const int all = (a.H[m] + U * kRows - 1) / (U * kRows);
+        n_sets[m] = (all - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y;
+    }
+    auto step = [&](int &bb, int &tt) {
+        bb += step_b;
+        tt += step_t;
+        if (tt >= a.T_) {
+            tt -= a.T_;
+            ++bb;
+        }
+    };
+    // the set to be loaded next: its token, how many of its tensor are left, its first head
+    // and rows
+    int lb = b, lt = t, l_left = n_sets[0] + n_sets[1] > 0 ? left : 0, lm = n_sets[0] > 0 ? 0 : 1, li = 0, lh = 0;
+    const T *lx = nullptr, *lg = nullptr;
+    uint32_t l_at = ring_at;
+    auto load_tensor = [&]() {  // the first set of the token's tensor lm
+        li = n_sets[lm];
+        lh = (int)blockIdx.y * (U * kRows);
+        lx = a.x[lm] + lb * a.sb[lm] + lt * a.st[lm] + (lh + sub) * a.sh[lm] + L.o0;
+        if (BWD) lg = a.gy[lm] + (((long long)lb * a.H[lm] + lh + sub) * a.T_ + lt) * D + L.o0;
+    };
+    if (l_left > 0) load_tensor();
+    const int run = L.o1 - L.o0;
+    const long long yh = (long long)a.T_ * D * kRows;
+    auto load_next = [&]() {
+        if (l_left > 0) {
+            const long long sh = a.sh[lm] * kRows;
+            const int H = a.H[lm];
+            if (lh + U * kRows <= H) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const T *x = lx + u * sh;
+                    async_copy<V>(l_at + (u * 2 * X) * (32 * V), x);
+                    async_copy<V>(l_at + (u * 2 * X + 1) * (32 * V), x + run);
+                    if (BWD) {
+                        const T *g = lg + u * yh;
+                        async_copy<V>(l_at + (u * 2 * X + 2) * (32 * V), g);
+                        async_copy<V>(l_at + (u * 2 * X + 3) * (32 * V), g + run);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const bool on = lh + u * kRows + sub < H;
+                    const T *x = on ? lx + u * sh : a.x[lm];
+                    async_copy<V>(l_at + (u * 2 * X) * (32 * V), x, on);
+                    async_copy<V>(l_at + (u * 2 * X + 1) * (32 * V), on ? x + run : x, on);
+                    if (BWD) {
+                        const T *g = on ? lg + u * yh : a.gy[lm];
+                        async_copy<V>(l_at + (u * 2 * X + 2) * (32 * V), g, on);
+                        async_copy<V>(l_at + (u * 2 * X + 3) * (32 * V), on ? g + run : g, on);
+                    }
+                }
+            }
+            if (--li > 0) {
+                lh += gridDim.y * (U * kRows);
+                lx += gridDim.y * (U * sh);
+                if (BWD) lg += gridDim.y * (U * yh);
+            } else {
+                if (lm == 0 && n_sets[1] > 0) {
+                    lm = 1;
+                } else {
+                    lm = n_sets[0] > 0 ? 0 : 1;
+                    step(lb, lt);
+                    --l_left;
+                }
+                if (l_left > 0) load_tensor();
+            }
+        }
+        async_commit();
+        l_at = l_at == ring_at + (kNormStages - 1) * kSetBytes ? ring_at : l_at + kSetBytes;
+    };
+#pragma unroll
+    for (int x = 0; x < kNormStages - 1; ++x) load_next();
+    uint32_t r_at = ring_at;  // the stage read
     auto position = [&](int bb, int tt) { return a.pos ? a.pos[bb * a.pos_stride + tt] : (long long)tt; };
     long long pos = left > 0 ? position(b, t) : 0;
     for (; left > 0; --left) {
         share_angles(cs_buf[warp], lane, pos, turn_freq, a.n_rot);
         // the next token's place and position, a token ahead
-        int nb = b + step_b, nt = t + step_t;
-        if (nt >= a.T_) {
-            nt -= a.T_;
-            ++nb;
-        }
+        int nb = b, nt = t;
+        step(nb, nt);
         if (left > 1) pos = position(nb, nt);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const int H = a.H[m];
-            if (H == 0) continue;
+            if (n_sets[m] <= 0) continue;
             const float4 u0 = *reinterpret_cast<const float4 *>(&cs_buf[warp][L.p0]);
             const float4 u1 = *reinterpret_cast<const float4 *>(&cs_buf[warp][L.p0 + 2]);
             const float2 cs[4] = {{u0.x, u0.y}, {u0.z, u0.w}, {u1.x, u1.y}, {u1.z, u1.w}};
@@ -352,72 +470,55 @@ norm_rotate_kernel(const NormArgs<T> a) {
             const Pairs w = gains(w_buf[m], L);
             Pairs fm, fk;
             if (!BWD) fold(turn, w, fm, fk);
-            const int h0 = blockIdx.y * (U * kRows) + sub, stride = gridDim.y * (U * kRows);
-            const long long sh = a.sh[m] * kRows, yh = (long long)a.T_ * D * kRows;
-            const T *px = a.x[m] + b * a.sb[m] + t * a.st[m] + h0 * a.sh[m];
-            const long long y0 = (((long long)b * H + h0) * a.T_ + t) * D;
-            T *po = BWD ? a.dx[m] + b * a.db[m] + t * a.dt[m] + h0 * a.dh[m] : a.y[m] + y0;
-            const long long oh = BWD ? a.dh[m] * kRows : yh;
-            const T *pg = BWD ? a.gy[m] + y0 : nullptr;
-            auto work = [&](const Row &rx, const Row &rg, T *dst, bool on) {
-                Pairs o;
-                if constexpr (BWD)
-                    o = row_backward<D>(rx.get(), rg.get(), turn, w, dw[m], a.eps);
-                else
-                    o = row_forward<D>(rx.get(), fm, fk, a.eps);
-                if (on) Row::store(dst, L.o0, L.o1, o);
-            };
-            int h = h0;
-            for (; h - sub + U * kRows <= H; h += stride) {
-                Row rx[U], rg[BWD ? U : 1];
+            int h = blockIdx.y * (U * kRows);
+            const long long oh = BWD ? a.dh[m] * kRows : (long long)a.T_ * D * kRows;
+            T *po = BWD ? a.dx[m] + b * a.db[m] + t * a.dt[m] + (h + sub) * a.dh[m]
+                        : a.y[m] + (((long long)b * H + h + sub) * a.T_ + t) * D;
+            for (int i = 0; i < n_sets[m]; ++i) {
+                load_next();
+                async_wait<kNormStages - 1>();
+                auto work = [&](int u, bool on) {
+                    Row rx, rg;
+                    rx.load_shared(r_at + (u * 2 * X) * (32 * V), r_at + (u * 2 * X + 1) * (32 * V));
+                    Pairs o;
+                    if constexpr (BWD) {
+                        rg.load_shared(r_at + (u * 2 * X + 2) * (32 * V), r_at + (u * 2 * X + 3) * (32 * V));
+                        o = row_backward<D>(rx.get(), rg.get(), turn, w, dw[m], a.eps);
+                    } else {
+                        o = row_forward<D>(rx.get(), fm, fk, a.eps);
+                    }
+                    if (on) Row::store(po + u * oh, L.o0, L.o1, o);
+                };
+                if (h + U * kRows <= H) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    rx[u].load(px + u * sh, L.o0, L.o1);
-                    if (BWD) rg[u].load(pg + u * yh, L.o0, L.o1);
+                    for (int u = 0; u < U; ++u) work(u, true);
+                } else {
+                    for (int u = 0; u < U && h + u * kRows < H; ++u) work(u, h + u * kRows + sub < H);
                 }
-#pragma unroll
-                for (int u = 0; u < U; ++u) work(rx[u], rg[BWD ? u : 0], po + u * oh, true);
-                px += gridDim.y * (U * sh);
+                r_at = r_at == ring_at + (kNormStages - 1) * kSetBytes ? ring_at : r_at + kSetBytes;
+                h += gridDim.y * (U * kRows);
                 po += gridDim.y * (U * oh);
-                if (BWD) pg += gridDim.y * (U * yh);
-            }
-            // the set of groups that reaches past the last head, if it is this block's
-            for (int u = 0; u < U && h - sub < H; ++u, h += kRows) {
-                Row rx, rg;
-                const bool on = h < H;
-                rx.zero();
-                rg.zero();
-                if (on) {
-                    rx.load(px, L.o0, L.o1);
-                    if (BWD) rg.load(pg, L.o0, L.o1);
-                }
-                work(rx, rg, po, on);
-                px += sh;
-                po += oh;
-                if (BWD) pg += yh;
             }
         }
         b = nb;
         t = nt;
     }
+    async_wait<0>();
     if constexpr (BWD)
         store_dw(dw, L, a.partial + ((long long)blockIdx.y * gridDim.x + blockIdx.x) * (2 * D));
 }
 
 // The same for few heads: a warp takes G row groups of each tensor at once, which are
 // all heads of a token, or with one group those of several consecutive tokens, 2^hs
-// rows to a token.  All loads are issued together, before the angles (each lane works
-// out its own four), or a token ahead where the registers hold it: the kernel above
-// waits for the angles, the queries and the keys of a token one after the other.
-// Forward / gradient of 60000 tokens, us, above and so: 8 + 8 heads of 64 80 / 104 and
-// 55 / 92, 6 + 3 heads 61 / 100 and 47 / 76, 12 + 12 heads (four groups) 111 / 155 and
-// 84 / 209, 16 + 16 heads 94 / 180 and 100 / 254; 171680 tokens of 2 + 2 heads 113 / 195
-// and 49 / 70.
+// rows to a token.  A token's rows are loaded together, a turn ahead, and each lane
+// works out its own four angles.  Forward / gradient of 60000 tokens, us, above and so: 2
+// groups, 8 + 8 heads of 64, 68 / 79 and 51 / 87 (so the gradient is not done so), 6 + 3 heads
+// 62 / 79 and 45 / 71, 16 + 16 heads of 32 67 / 79 and 51 / 83; 1 group, 4 + 4 heads of 64, 56 / 70 and
+// 35 / 50.  4 groups, 12 + 12 heads, take 82 us above and 80 so.
 template <typename T, int D, bool INTER, bool BWD, int G>
 __global__ void __launch_bounds__(32 * kNormWarps, 2)
 norm_rotate_packed_kernel(const NormArgs<T> a, int hs) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-    constexpr bool AHEAD = BWD ? G == 1 : G * sizeof(T) <= 8;
     using Row = Row8<T, INTER>;
     __shared__ float w_buf[2][D];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, sub = lane / kLanes;
@@ -459,7 +560,7 @@ norm_rotate_packed_kernel(const NormArgs<T> a, int hs) {
             }
     };
     Data d;
-    if (AHEAD && tok < a.tokens) load(b, t, mine < a.tokens, d);
+    if (tok < a.tokens) load(b, t, mine < a.tokens, d);
     for (; tok < a.tokens; tok += step) {
         int nb = b + step_b, nt = t + step_t;
         if (nt >= a.T_) {
@@ -468,10 +569,7 @@ norm_rotate_packed_kernel(const NormArgs<T> a, int hs) {
         }
         const long long at = tok + (sub >> hs);
         Data n;
-        if (AHEAD)
-            load(nb, nt, at + step < a.tokens, n);
-        else
-            load(b, t, at < a.tokens, d);
+        load(nb, nt, at + step < a.tokens, n);
         float2 cs[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -501,7 +599,7 @@ norm_rotate_packed_kernel(const NormArgs<T> a, int hs) {
                 }
             }
         }
-        if (AHEAD) d = n;
+        d = n;
         b = nb;
         t = nt;
     }
@@ -536,13 +634,12 @@ norm_dw_kernel(const float *partial, int n, float *dwq, float *dwk) {
 int max_heads(const NormRotate &p) { return p.H[0] > p.H[1] ? p.H[0] : p.H[1]; }
 
 // log2 of the rows that a token takes in the packed kernel; -1: too many heads for it.
-// The forward takes up to four groups, but four full ones go faster above (the figures
-// are at the kernel), the gradient two, by its registers.
+// The forward takes two row groups, the gradient one (the figures are at the kernel).
 int norm_packed(const NormRotate &p) {
     const int hm = max_heads(p), rows = 256 / p.d;
     int hs = 0;
     while ((1 << hs) < hm && (1 << hs) < rows) ++hs;
-    return hm <= (p.backward ? 2 * rows : 4 * rows - 1) ? hs : -1;
+    return hm <= (p.backward ? rows : 2 * rows) ? hs : -1;
 }
 
 template <typename T, int D, bool INTER, bool BWD>
@@ -574,15 +671,15 @@ cudaError_t launch_one(const NormRotate &p, cudaStream_t st) {
     {
         ProfScope prof(BWD ? "norm_rotate_bwd" : "norm_rotate", st);
         const int hs = norm_packed(p);
-        const int groups = (max_heads(p) + 256 / D - 1) / (256 / D);
-        if (hs >= 0 && groups == 1)
+        if (hs >= 0 && max_heads(p) <= 256 / D)
             norm_rotate_packed_kernel<T, D, INTER, BWD, 1><<<grid, 32 * kNormWarps, 0, st>>>(a, hs);
-        else if (hs >= 0 && (BWD || groups == 2))
-            norm_rotate_packed_kernel<T, D, INTER, BWD, 2><<<grid, 32 * kNormWarps, 0, st>>>(a, hs);
         else if (!BWD && hs >= 0)
-            norm_rotate_packed_kernel<T, D, INTER, false, 4><<<grid, 32 * kNormWarps, 0, st>>>(a, hs);
-        else
-            norm_rotate_kernel<T, D, INTER, BWD><<<grid, 32 * kNormWarps, 0, st>>>(a);
+            norm_rotate_packed_kernel<T, D, INTER, false, 2><<<grid, 32 * kNormWarps, 0, st>>>(a, hs);
+        else {
+            const cudaError_t e = smem_opt_in_once<norm_rotate_kernel<T, D, INTER, BWD>>(kNormRing);
+            if (e != cudaSuccess) return e;
+            norm_rotate_kernel<T, D, INTER, BWD><<<grid, 32 * kNormWarps, kNormRing, st>>>(a);
+        }
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !BWD || (!p.dw[0] && !p.dw[1])) return e;
