@@ -19,11 +19,11 @@
 // The register-level products (mma.sync) suit tiles this small, whose split takes
 // the arithmetic of all the warps: tcgen05 would need the three planes of the
 // weights in tensor memory beside their scores, 192 columns where a step of the bf16
-// kernel has 128.  Measured (8 heads, 2048 queries and keys, d = 64): forward 158 us,
-// dq 220 us, dkv 288 us, which is 54, 58 and 60 TFLOP/s of fp32 products (the CUDA
-// cores' form of this kernel: 279, 394, 521 us, bound by its shared-memory reads);
-// bound by the register-level products, whose pipe is 66 to 74% active at 543
-// TFLOP/s of bf16 products / 6.
+// kernel has 128.  Measured (8 heads, 2048 queries and keys, d = 64): forward 159 us,
+// gradient 485 us, which is 54 and 62 TFLOP/s of fp32 products (the CUDA cores' form of
+// this kernel: 279 and 915 us, bound by its shared-memory reads); bound by the
+// register-level products, whose pipe is 66 to 74% active.  (With twice as many chains of
+// products side by side: the same.)
 #include <cuda_bf16.h>
 
 #include "kata_internal.cuh"
@@ -67,21 +67,38 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &h, uint32_t &
     l = pack_bf16x2(x, y);
 }
 
-// 64 rows of D floats into three planes, rows from `live` on as zeros.
-template <int D>
-__device__ __forceinline__ void load_planes(uint8_t *dst, const float *src, int live) {
-#pragma unroll 4
-    for (int x = threadIdx.x; x < kN * (D / 4); x += kThreads) {
-        const int r = x / (D / 4), c = x % (D / 4);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < live) v = *reinterpret_cast<const float4 *>(src + (long long)r * D + 4 * c);
-        uint2 p[3];
-        split2(v.x, v.y, p[0].x, p[1].x, p[2].x);
-        split2(v.z, v.w, p[0].y, p[1].y, p[2].y);
-        const uint32_t o = at(r, c / 2) + 8 * (c & 1);
+// N times 64 rows of D floats into three planes each, rows from `live` on as zeros.  All
+// loads are issued before the first is split: the wait for memory is the same for one
+// operand and for four.
+struct Source {
+    uint8_t *dst;
+    const float *src;
+    int live;
+};
+template <int D, int N>
+__device__ __forceinline__ void load_planes(const Source (&op)[N]) {
+    constexpr int K = kN * (D / 4) / kThreads;
+    float4 v[N][K];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2 *>(dst + i * kPlane + o) = p[i];
-    }
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int x = threadIdx.x + k * kThreads, r = x / (D / 4), c = x % (D / 4);
+            v[n][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < op[n].live) v[n][k] = *reinterpret_cast<const float4 *>(op[n].src + (long long)r * D + 4 * c);
+        }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int x = threadIdx.x + k * kThreads, r = x / (D / 4), c = x % (D / 4);
+            uint2 p[3];
+            split2(v[n][k].x, v[n][k].y, p[0].x, p[1].x, p[2].x);
+            split2(v[n][k].z, v[n][k].w, p[0].y, p[1].y, p[2].y);
+            const uint32_t o = at(r, c / 2) + 8 * (c & 1);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2 *>(op[n].dst + i * kPlane + o) = p[i];
+        }
 }
 
 __device__ __forceinline__ void ldm(uint32_t (&r)[4], uint32_t addr) {
@@ -212,10 +229,6 @@ __device__ __forceinline__ void cross_f32(const FArgs &a, int cta, uint8_t *sm) 
 
     float acc0[D / 8][4] = {}, acc1[MODE == kCrossDkv ? D / 8 : 1][4] = {};
     float l[2] = {0.f, 0.f}, delta[2] = {0.f, 0.f};  // of rows w0 + g and w0 + g + 8
-    if (b0 < b1) {
-        load_planes<D>(R0, a.r0 + row0 * D, rows - r0);
-        if (MODE != kCrossFwd) load_planes<D>(R1, a.r1 + row0 * D, rows - r0);
-    }
     if (MODE == kCrossDq) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -225,9 +238,15 @@ __device__ __forceinline__ void cross_f32(const FArgs &a, int cta, uint8_t *sm) 
     }
     for (int b = b0; b < b1; ++b) {
         const int c0 = b * kN;
+        const Source s0 = {C0, a.c0 + (col0 + c0) * D, cols - c0}, s1 = {C1, a.c1 + (col0 + c0) * D, cols - c0};
         __syncthreads();  // the last block's operands are read
-        load_planes<D>(C0, a.c0 + (col0 + c0) * D, cols - c0);
-        load_planes<D>(C1, a.c1 + (col0 + c0) * D, cols - c0);
+        if (b > b0) {
+            load_planes<D>({s0, s1});
+        } else if constexpr (MODE == kCrossFwd) {
+            load_planes<D>({{R0, a.r0 + row0 * D, rows - r0}, s0, s1});
+        } else {
+            load_planes<D>({{R0, a.r0 + row0 * D, rows - r0}, {R1, a.r1 + row0 * D, rows - r0}, s0, s1});
+        }
         if (MODE == kCrossDkv && threadIdx.x < kN) {
             sd[threadIdx.x] = a.delta[(long long)bh * a.stat_stride + c0 + threadIdx.x];
             sr[threadIdx.x] = a.rden[(long long)bh * a.stat_stride + c0 + threadIdx.x];
