@@ -224,6 +224,21 @@ def test_few_terms_keep_their_precision(H, Hk, Tq, Tk, d):
         assert O.worst(a, r, b) <= 1
 
 
+def test_few_terms_with_masked_keys_of_any_content():
+    q, k, v, g = make(3, 4, 2, 70, 29, 64, "bf16", 5)
+    n = lens(17, 0, 1)
+    for b, x in enumerate((17, 0, 1)):
+        k[b, :, x:], v[b, :, x:] = float("nan"), float("-inf")
+    out, y, den = forward(q, k, v, n)
+    got = K.kata_cross_backward(g, q, k, v, y, den, key_lengths=n)
+    kk, vv = k.clone(), v.clone()
+    for b, x in enumerate((17, 0, 1)):
+        kk[b, :, x:], vv[b, :, x:] = 0, 0
+    assert not out[1].any() and not got[0][1].any()
+    for a, r, b in zip(got, O.cross_grad(g, q, kk, vv, n), O.cross_bounds(q, kk, vv, q.dtype, n, dout=g, split=True)):
+        assert O.worst(a, r, b) <= 1
+
+
 @pytest.mark.parametrize("Tq,Tk", [(257, 700), (40, 4000), (1000, 33)])
 def test_query_gradient_of_the_smallest_heads_keeps_its_precision(Tq, Tk):
     q, k, v, g = make(2, 4, 2, Tq, Tk, 16, "bf16", Tq)
