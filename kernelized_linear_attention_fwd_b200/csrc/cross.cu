@@ -178,12 +178,17 @@ __device__ void cut_join(const CutJob<T> &j) {
     const int slot0 = 2 * (c - 1) + (same ? 0 : 1);  // the item began that CTA's stretch, or ended it
     int n = 2;                                       // pieces
     if (!me.last)
-        for (int x = c + 1;; x += 32) {  // up to the CTA that reaches the item's end
-            const bool end = x + lane >= grid || pieces[x + lane].last;
-            const unsigned m = __ballot_sync(0xffffffffu, end);
-            if (m) {
-                n = x + __ffs(m) - c + 1;
-                break;
+        for (int x = c + 1, k = 4; k == 4; x += 128) {  // up to the CTA that reaches the item's end
+            bool end[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) end[i] = x + 32 * i + lane >= grid || pieces[x + 32 * i + lane].last;
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                const unsigned m = __ballot_sync(0xffffffffu, end[i]);
+                if (m) {
+                    n = x + 32 * i + __ffs(m) - c + 1;
+                    k = i;
+                }
             }
         }
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, g = ty % G16, col = 4 * tx;
@@ -194,7 +199,7 @@ __device__ void cut_join(const CutJob<T> &j) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
     if (on) {
-#pragma unroll 4
+#pragma unroll 8
         for (int x = g; x < n; x += G16) {
             const long long pr = (x == 0 ? slot0 : 2LL * (c - 1 + x)) * s.slot_rows + row;
             const float4 w = *reinterpret_cast<const float4 *>(part + pr * d + col);

@@ -99,7 +99,8 @@ struct XBars {
 
 // SPLIT: what goes back into the products (w, ds, w / l) as two bf16 numbers each, a
 // high and a low part, which takes twice the products that accumulate.  Used by
-// training steps (CrossPlan::split) where the rounding of one number would show:
+// training steps (CrossPlan::split) where the rounding of one number would show, and by
+// the forward of few rows:
 //
 // - The forward, d <= 32: its y gives the backward pass D = dy.y, and an error of D
 //   enters every key's gradient with one sign: next to the other roundings it is as
@@ -111,6 +112,7 @@ struct XBars {
 //   rounding), without, 0.0017 with it.
 // - dq and dkv with up to 32 rows or 32 keys: few roundings enter a sum, and with two
 //   keys, say, p and D cancel (1.6 to 2.4 times the output's own rounding without).
+// - Any forward of up to 32 rows: outputs so few show single roundings.
 template <int MODE, int GROUPS, bool SPLIT>
 __device__ __forceinline__ void cross_tc(const CUtensorMap &tm_r0, const CUtensorMap &tm_r1, const CUtensorMap &tm_c0,
                                          const CUtensorMap &tm_c1, const XArgs &a, int cta) {
@@ -574,7 +576,8 @@ cudaError_t launch_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t 
 }  // namespace
 
 cudaError_t launch_cross_tc_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
-    return io.y && p.split[kCrossFwd] ? launch_mode<kCrossFwd, true>(p, io, st) : launch_mode<kCrossFwd, false>(p, io, st);
+    const bool split = io.y ? p.split[kCrossFwd] : p.R <= kSplitRows;
+    return split ? launch_mode<kCrossFwd, true>(p, io, st) : launch_mode<kCrossFwd, false>(p, io, st);
 }
 cudaError_t launch_cross_tc_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     if (p.split[kCrossDkv]) return launch_backward<true, true>(p, io, st);

@@ -274,10 +274,11 @@ struct CrossIo {
 inline int cross_whole(const XSched &s, const CrossIo &io) { return s.whole == 2 || (s.whole && !io.key_lengths); }
 cudaError_t launch_cross_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 cudaError_t launch_cross_backward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
-// One mode's main kernel: forward of at most kFewRows rows per key head; others in
-// bf16 and in fp32.
-constexpr int kFewRows = 4;
-// CTAs per SM of that kernel for this many rows (64, 80, 128 registers a thread).
+// One mode's main kernel: forward of at most kFewRows (bf16: kFewRowsBf16) rows per key
+// head; others in bf16 and in fp32.
+constexpr int kSplitRows = 32;  // bf16: up to so many rows or keys, operands as two bf16 numbers
+constexpr int kFewRows = 4, kFewRowsBf16 = 16;
+// CTAs per SM of those kernels for this many rows (64, 80, 128 registers a thread).
 __host__ __device__ constexpr int few_per_sm(int rows) { return rows == 1 ? 4 : rows == 2 ? 3 : 2; }
 cudaError_t launch_cross_few(const CrossPlan &p, const CrossIo &io, cudaStream_t st);
 cudaError_t launch_cross_tc_forward(const CrossPlan &p, const CrossIo &io, cudaStream_t st);

@@ -218,7 +218,7 @@ kata_status cross_plan(int B, int H, int Hkv, int Tq, int Tk, int d, kata_dtype 
     p.ws_delta = 0;
     p.ws_rden = stat;
     size_t off = 2 * stat;
-    p.few = p.R <= kFewRows;
+    p.few = p.R <= (dtype == KATA_BF16 ? kFewRowsBf16 : kFewRows);
     // dq and dkv in one launch while each would take an SM less than some 32 steps; the
     // SMs go by the steps' times, about 1 : 1.4
     const long long rt = (p.R + kXTile - 1) / kXTile, kt = (Tk + kXTile - 1) / kXTile;
@@ -228,7 +228,7 @@ kata_status cross_plan(int B, int H, int Hkv, int Tq, int Tk, int d, kata_dtype 
     // forward of heads up to 32 or of few keys (256 keys: 57 us, 66 so, for 3 sequences of
     // 16 heads and 4000 queries), dq of heads of 16, everything if few rows meet in a
     // sum (16 rows on 4000 keys, 48 heads: backward 79 us, 89 so).
-    const bool few_terms = p.R <= 32 || Tk <= 32;
+    const bool few_terms = p.R <= kSplitRows || Tk <= kSplitRows;
     p.split[kCrossFwd] = d <= 32 || Tk <= 256 || few_terms;
     p.split[kCrossDq] = d == 16 || few_terms;
     p.split[kCrossDkv] = few_terms;

@@ -165,6 +165,26 @@ def test_single_token_against_a_long_memory(dtype, B, H, Hk, Tk):
     check(q, k, v, g, torch.randint(1, Tk, (B,), device="cuda").int())
 
 
+@pytest.mark.parametrize("d", [16, 32, 64])
+@pytest.mark.parametrize("H,Hk,Tq,Tk", [(5, 1, 1, 3000), (8, 1, 1, 1), (16, 2, 1, 20000), (16, 1, 1, 127), (6, 3, 4, 129),
+                                        (2, 2, 13, 16), (3, 3, 16, 700), (17, 1, 1, 900), (2, 2, 32, 5000)])
+def test_steps_of_several_rows(H, Hk, Tq, Tk, d):
+    # up to 32 rows a key head in bf16: errors are the outputs' rounding
+    q, k, v, g = make(3, H, Hk, Tq, Tk, d, "bf16", seed=Tk + d)
+    for n in (None, lens(Tk, 0, (Tk + 1) // 2)):
+        kk, vv = k.clone(), v.clone()
+        if n is not None:
+            for b in range(3):
+                kk[b, :, int(n[b]):], vv[b, :, int(n[b]):] = float("nan"), float("inf")
+        out, y, den = forward(q, kk, vv, n)
+        ref, l = O.cross(q, k, v, n)
+        bo, by = O.cross_bounds(q, k, v, q.dtype, n, split=True)
+        assert O.worst(out, ref, bo) <= 1 and O.worst(y, ref, by) <= 1
+        # without the exports the same kernel
+        assert torch.equal(out, K.kata_cross_forward(q, kk, vv, key_lengths=n))
+    check(q, k, v, g, lens(Tk, 0, (Tk + 1) // 2))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_many_queries_on_few_keys(dtype):
     # the queries are split over the SMs for dk and dv
