@@ -488,9 +488,9 @@ kata_status kata_qk_norm_rotate_backward(
  * numbers, and so in kata_cross_backward).  KATA_F32
  * keeps fp32 accuracy: its products are sums of products of three bf16 numbers per
  * operand (24 bits; for magnitudes between 2^-100 and 2^127, and not-a-number where
- * an infinity is visible).  At most 4 rows per key head ((H / Hkv) * Tq, a decode step)
- * run in fp32 on the CUDA cores for either type; the weights of up to 32 rows in bf16
- * are sums of two bf16 numbers with or without y_out.
+ * an infinity is visible).  At most 2 rows per key head ((H / Hkv) * Tq, a decode step),
+ * in fp32 4, run in fp32 on the CUDA cores; the weights of up to 32 rows in bf16 are sums
+ * of two bf16 numbers with or without y_out.
  *
  * kata_cross_backward: with dout the gradient of out and D_t = dout_t.y_t,
  *

@@ -1,6 +1,6 @@
 // Cross attention forward for few rows per key head (decode steps), on the register
-// level: y = sum_s w v / sum_s w, w = (q.k)^2.  Up to 4 rows, bf16 and fp32, on the CUDA
-// cores; 5 to 16 rows in bf16 by register-level tensor products (further down).
+// level: y = sum_s w v / sum_s w, w = (q.k)^2.  Up to 2 rows in bf16 and 4 in fp32 on
+// the CUDA cores; 3 to 16 rows in bf16 by register-level tensor products (further down).
 //
 // Bound by reading the keys and values once.  64 sequences of 1501 keys and less, 16
 // heads, one query (270 MB): 45 us, 6.0 TB/s, against 60 us on the tensor cores, whose
@@ -107,7 +107,7 @@ __device__ __forceinline__ void few_end(const FArgs &a, const XItem &it, const f
     }
 }
 
-// RB: rows computed (the rows rounded up to 1, 2, 4).
+// RB: rows computed (the rows rounded up to 1, 2, and in fp32 4).
 template <typename T, int D, int RB>
 __global__ void __launch_bounds__(32 * kFWarps, few_per_sm(RB))
 cross_few_kernel(const FArgs a) {
@@ -209,7 +209,7 @@ cross_few_kernel(const FArgs a) {
     }
 }
 
-// Five to 16 rows (decode steps with shared key heads), bf16: the products are
+// Three to 16 rows (decode steps with shared key heads), bf16: the products are
 // register-level ones (m16n8k16), whose 16 rows are the rows, so that a key's operands go from
 // memory to registers once and stay there.  A lane loads D / 4 coordinates of a key, in
 // one run; the coordinates' order within a product is free, so these words are the score
@@ -218,14 +218,16 @@ cross_few_kernel(const FArgs a) {
 // both.  A warp has 16 keys of the next block in flight while it works on one.  2 key heads
 // of 131072 keys, 8 rows (67 MB): 12.1 us, 5.5 TB/s, and 6 for the join of 296 pieces; on the
 // 128-row tiles 15.5 and 4.7 with the weights as precise.  One CTA of 16 warps per SM: 18 us.
+// 4 rows on 64 x 4 key heads of 1500 keys (98 MB), with the join: 35 us on the CUDA cores, 27
+// so; 1 and 2 rows are 5% slower so.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -360,8 +362,7 @@ template <typename T, int D>
 cudaError_t launch_d(const CrossPlan &p, const CrossIo &io, cudaStream_t st) {
     if (p.R == 1) return launch_rb<T, D, 1>(p, io, st);
     if (p.R == 2) return launch_rb<T, D, 2>(p, io, st);
-    if (sizeof(T) == 2 && p.R > kFewRows) return launch_rb<__nv_bfloat16, D, 16>(p, io, st);
-    return launch_rb<T, D, 4>(p, io, st);
+    return launch_rb<T, D, sizeof(T) == 2 ? 16 : 4>(p, io, st);
 }
 
 template <typename T>
