@@ -152,7 +152,7 @@ def test_cross_backward_refusals(lib, bad, status):
     assert cross(lib, "b", **bad) == status
 
 
-def test_norm_workspace(lib):
+def test_norm_workspace_limits(lib):
     W = lib.kata_qk_norm_rotate_backward_workspace_bytes
     top = 2 ** 31 - 2 ** 17
     assert W(1, top - 1, 1, 1, 64) > 0 and W(top - 1, 1, 1, 1, 64) > 0
