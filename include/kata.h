@@ -434,7 +434,9 @@ kata_status kata_decode_step_packed(const void *q, const void *k, const void *v,
  * kata_qk_norm_rotate_backward: the gradient.  dq_out, dk_out are the gradients
  * of q_out and k_out (dense, head-major); dq, dk receive those of q and k with
  * strides of their own (no two rows may share memory; dq and dk may be
- * slices of one fused buffer); dq_weight, dk_weight (nullable, fp32 [d]) those
+ * slices of one fused buffer, whatever its order of batch, tokens and heads;
+ * where the strides do not tell that the rows lie apart, KATA_ERR_INVALID_ARG);
+ * dq_weight, dk_weight (nullable, fp32 [d]) those
  * of the gains, summed over all rows in a fixed order.  The workspace is
  * kata_qk_norm_rotate_backward_workspace_bytes(...) bytes, 256-byte aligned.
  * dq and dk must not overlap any input.

@@ -54,44 +54,76 @@ size_t norm_span(const NormRotate &p, int m, const long long (&s)[3]) {
     return (size_t)e * (p.dtype == KATA_BF16 ? 2 : 4);
 }
 
-// No two rows share memory: sorted by stride, every axis steps over all that the
-// shorter ones cover.
-bool rows_disjoint(const NormRotate &p, int m, const long long (&s)[3]) {
-    long long n[3] = {p.B, p.T, p.H[m]}, t[3] = {s[0], s[1], s[2]};
-    for (int i = 0; i < 3; ++i)
-        for (int j = i + 1; j < 3; ++j)
-            if (t[j] < t[i]) {
-                const long long a = t[i], b = n[i];
-                t[i] = t[j];
-                n[i] = n[j];
-                t[j] = a;
-                n[j] = b;
-            }
-    long long cover = p.d;
+// A strided box of rows, its axes by falling stride.
+struct Rows {
+    long long s[3], n[3];
+    int axes = 0;
+    long long d;
+    // elements from the first to behind the last, of the axes from `i` on
+    long long span(int i) const {
+        long long e = d;
+        for (; i < axes; ++i) e += (n[i] - 1) * s[i];
+        return e;
+    }
+};
+Rows rows_of(const NormRotate &p, int m, const long long (&s)[3]) {
+    const long long n[3] = {p.B, p.T, p.H[m]};
+    Rows r;
+    r.d = p.d;
     for (int i = 0; i < 3; ++i) {
         if (n[i] == 1) continue;
-        if (t[i] < cover) return false;
-        cover = (n[i] - 1) * t[i] + cover;
+        int k = r.axes++;
+        for (; k > 0 && r.s[k - 1] < s[i]; --k) {
+            r.s[k] = r.s[k - 1];
+            r.n[k] = r.n[k - 1];
+        }
+        r.s[k] = s[i];
+        r.n[k] = n[i];
     }
+    return r;
+}
+
+// No two rows share memory: every axis steps over all that the shorter ones cover.
+bool rows_disjoint(const Rows &r) {
+    for (int i = 0; i < r.axes; ++i)
+        if (r.s[i] < r.span(i + 1)) return false;
     return true;
 }
 
-// dq and dk: apart, or slices of one buffer that share the batch and token
-// strides, the heads of one lying between the tokens of the other.
+// No row of a (axes from i on) meets one of b (from j on), which starts `off` elements
+// behind it.  The longest step moves one against the other; where it belongs to both, only
+// the difference m of their places on it counts: off + m step.  Each place at which the
+// rest of the two could meet is looked into.  With rows that do not overlap themselves
+// there are two at most on a shared step; a box that meets more of the other's steps is
+// taken for overlapping.
+bool boxes_apart(const Rows &a, int i, const Rows &b, int j, long long off) {
+    if (off >= a.span(i) || -off >= b.span(j)) return true;
+    if (i == a.axes && j == b.axes) return false;
+    const long long sa = i < a.axes ? a.s[i] : 0, sb = j < b.axes ? b.s[j] : 0, step = sa > sb ? sa : sb;
+    if (step < 1) return false;
+    const int ia = i + (sa == step), jb = j + (sb == step);
+    // they can meet for -eb < off + m step < ea
+    const long long ea = a.span(ia), eb = b.span(jb);
+    auto floor_div = [](long long x, long long y) { return x >= 0 ? x / y : -((y - 1 - x) / y); };
+    long long lo = floor_div(-eb - off, step) + 1, hi = floor_div(ea - 1 - off, step);
+    const long long m0 = ia > i ? 1 - a.n[i] : 0, m1 = jb > j ? b.n[j] - 1 : 0;
+    if (lo < m0) lo = m0;
+    if (hi > m1) hi = m1;
+    if (hi - lo > 1) return false;
+    for (long long m = lo; m <= hi; ++m)
+        if (!boxes_apart(a, ia, b, jb, off + m * step)) return false;
+    return true;
+}
+
+// dq and dk (each without overlap of its own rows) share no row: in separate buffers, or
+// slices of one in whatever order of batch, tokens and heads.
 bool slices_disjoint(const NormRotate &p) {
-    const size_t n0 = norm_span(p, 0, p.ds[0]), n1 = norm_span(p, 1, p.ds[1]);
-    if (!overlaps(p.dx[0], n0, p.dx[1], n1)) return true;
-    for (int i = 0; i < 2; ++i)
-        if (p.ds[0][i] != p.ds[1][i]) return false;
     const long long es = p.dtype == KATA_BF16 ? 2 : 4;
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(p.dx[0]), a1 = reinterpret_cast<uintptr_t>(p.dx[1]);
     const int lo = a0 <= a1 ? 0 : 1;
-    const long long gap = (long long)(lo == 0 ? a1 - a0 : a0 - a1) / es;
-    const long long e_lo = (p.H[lo] - 1) * p.ds[lo][2] + p.d, e_hi = (p.H[1 - lo] - 1) * p.ds[1 - lo][2] + p.d;
-    long long step = 0;  // shortest of the shared steps in use
-    if (p.T > 1) step = p.ds[0][1];
-    if (p.B > 1 && (step == 0 || p.ds[0][0] < step)) step = p.ds[0][0];
-    return gap >= e_lo && (step == 0 || gap + e_hi <= step);
+    const uintptr_t gap = lo == 0 ? a1 - a0 : a0 - a1;
+    if (gap >= norm_span(p, lo, p.ds[lo])) return true;
+    return boxes_apart(rows_of(p, lo, p.ds[lo]), 0, rows_of(p, 1 - lo, p.ds[1 - lo]), 0, (long long)gap / es);
 }
 
 // Checks shared by both directions; y of the backward pass are the gradients.
@@ -349,7 +381,7 @@ kata_status kata_qk_norm_rotate_backward(const void *dq_out, const void *dk_out,
         p.gy[m] = gy[m];
         p.dx[m] = dx[m];
         p.dw[m] = dw[m];
-        if (p.x[m] && (!norm_strides(p, m, ds[m], p.ds[m]) || !rows_disjoint(p, m, p.ds[m])))
+        if (p.x[m] && (!norm_strides(p, m, ds[m], p.ds[m]) || !rows_disjoint(rows_of(p, m, p.ds[m]))))
             return KATA_ERR_INVALID_ARG;
     }
     for (int m = 0; m < 2; ++m) {

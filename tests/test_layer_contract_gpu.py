@@ -1,0 +1,61 @@
+"""What include/kata.h promises of the head norm and of cross attention beyond their
+values on ordinary inputs: layouts of the gradients, zeros behind the last key whatever
+the queries hold."""
+from __future__ import annotations
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import kernelized_linear_attention_fwd_b200 as K  # noqa: E402
+from kernelized_linear_attention_fwd_b200.csrc import build as kbuild  # noqa: E402
+from tests.test_norm_rotate_gpu import freq  # noqa: E402
+from tests.test_norm_rotate_gpu import make as norm_make  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    kbuild.build()
+    K.load_library()
+    yield
+    assert K.kata_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,Hk", [(4, 2), (1, 1), (16, 4)])
+def test_gradients_as_slices_of_one_buffer_in_any_order(dtype, H, Hk):
+    B, T, d = 3, 37, 32
+    _, q, k = norm_make(B, T, H, Hk, d, dtype, 3)
+    kw = dict(inv_freq=freq(16))
+    yq, yk = K.kata_qk_norm_rotate(q, k, **kw)
+    gq, gk = torch.randn_like(yq), torch.randn_like(yk)
+    dq, dk, _, _ = K.kata_qk_norm_rotate_backward(gq, gk, q, k, **kw)
+    n = H + 2 * Hk
+    for order in ((0, 1, 2), (0, 2, 1), (1, 0, 2), (2, 0, 1)):  # of batch, token, head in memory
+        size = [(B, T, n)[x] for x in order] + [d]
+        back = [order.index(x) for x in range(3)] + [3]
+        buf = torch.full(size, 7.0, dtype=q.dtype, device="cuda")
+        view = buf.permute(back)  # [B, T, n, d]
+        K.kata_qk_norm_rotate_backward(gq, gk, q, k, dq=view[:, :, :H], dk=view[:, :, H:H + Hk], **kw)
+        assert torch.equal(view[:, :, :H], dq) and torch.equal(view[:, :, H:H + Hk], dk), order
+        assert bool((view[:, :, H + Hk:] == 7.0).all())
+    # queries, keys and values head by head
+    buf = torch.full((B, T, max(H, Hk), 3, d), 7.0, dtype=q.dtype, device="cuda")
+    K.kata_qk_norm_rotate_backward(gq, gk, q, k, dq=buf[:, :, :H, 0], dk=buf[:, :, :Hk, 1], **kw)
+    assert torch.equal(buf[:, :, :H, 0], dq) and torch.equal(buf[:, :, :Hk, 1], dk)
+    assert bool((buf[:, :, :, 2] == 7.0).all()) and bool((buf[:, :, Hk:, 1] == 7.0).all())
+
+
+def test_gradients_that_share_rows_are_refused():
+    _, q, k = norm_make(2, 2, 1, 1, 64, "bf16", 4)
+    g = torch.randn(2, 1, 2, 64, device="cuda").bfloat16()
+    buf = torch.full((1024,), 7.0, dtype=torch.bfloat16, device="cuda")
+    s = (192, 128, 64, 1)  # token 1 of sequence 0 of dk is token 0 of sequence 1 of dq
+    with pytest.raises(K.KataError):
+        K.kata_qk_norm_rotate_backward(g, g, q, k, dq=buf.as_strided(q.shape, s),
+                                       dk=buf[64:].as_strided(k.shape, s))
+    assert bool((buf == 7.0).all())
