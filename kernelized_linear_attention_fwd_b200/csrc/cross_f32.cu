@@ -310,15 +310,19 @@ __device__ __forceinline__ void cross_f32(const FArgs &a, int cta, uint8_t *sm) 
         float f = 1.f;
         if (!cut && MODE == kCrossFwd) f = cross_recip(l[i]);
         if (!cut && MODE == kCrossDq) f = 2.f * a.rden[(long long)bh * a.stat_stride + r];
+        // padded keys beside the last visible one: zeros, also where a query that is not finite
+        // turned their zero products into NaN (the length is read again: a register less above)
+        const bool dead = MODE == kCrossDkv && r >= cross_length(a.key_lengths, bh / a.Hkv, a.Tk);
         float *o = cut ? a.part + pr * D : a.o0 + gr * D;
         float *o1 = MODE == kCrossDkv ? (cut ? a.part + (pr + n_rows) * D : a.o1 + gr * D) : nullptr;
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) {
-            const float2 v = make_float2(acc0[j][2 * i] * f, acc0[j][2 * i + 1] * f);
+            const float2 v = dead ? make_float2(0.f, 0.f) : make_float2(acc0[j][2 * i] * f, acc0[j][2 * i + 1] * f);
             *reinterpret_cast<float2 *>(o + 8 * j + q) = v;
             if (MODE == kCrossFwd && !cut && a.y) *reinterpret_cast<float2 *>(a.y + gr * D + 8 * j + q) = v;
             if constexpr (MODE == kCrossDkv)
-                *reinterpret_cast<float2 *>(o1 + 8 * j + q) = make_float2(acc1[j][2 * i], acc1[j][2 * i + 1]);
+                *reinterpret_cast<float2 *>(o1 + 8 * j + q) =
+                    dead ? make_float2(0.f, 0.f) : make_float2(acc1[j][2 * i], acc1[j][2 * i + 1]);
         }
         if (MODE == kCrossFwd && q == 0) {
             if (cut)

@@ -13,6 +13,7 @@ if not torch.cuda.is_available():
 
 import kernelized_linear_attention_fwd_b200 as K  # noqa: E402
 from kernelized_linear_attention_fwd_b200.csrc import build as kbuild  # noqa: E402
+from tests.test_cross_gpu import forward, lens, make  # noqa: E402
 from tests.test_norm_rotate_gpu import freq  # noqa: E402
 from tests.test_norm_rotate_gpu import make as norm_make  # noqa: E402
 
@@ -59,3 +60,22 @@ def test_gradients_that_share_rows_are_refused():
         K.kata_qk_norm_rotate_backward(g, g, q, k, dq=buf.as_strided(q.shape, s),
                                        dk=buf[64:].as_strided(k.shape, s))
     assert bool((buf == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Tq,Tk", [(50, 300), (3000, 40), (40, 1000)])
+@pytest.mark.parametrize("where", ["query", "gradient"])
+def test_gradients_of_padded_keys_are_zero_whatever_the_queries_hold(dtype, Tq, Tk, where):
+    # one row that is not finite beside keys that end inside a tile: dk and dv of the
+    # keys from the length on are zero all the same
+    for d in (16, 64):
+        q, k, v, g = make(3, 4, 2, Tq, Tk, d, dtype, seed=Tk + d)
+        n = lens(Tk - 7, 0, Tk // 2 + 1)
+        for bad in (float("nan"), float("inf")):
+            (q if where == "query" else g)[:, 1, Tq // 2, 3] = bad
+            _, y, den = forward(q, k, v, n)
+            _, dk, dv = K.kata_cross_backward(g, q, k, v, y, den, key_lengths=n)
+            for b in range(3):
+                assert not dk[b, :, int(n[b]):].any() and not dv[b, :, int(n[b]):].any(), (d, bad, b)
+                # key head 1 has none of the bad row
+                assert bool(torch.isfinite(dk[b, 1]).all()) and bool(torch.isfinite(dv[b, 1]).all())
