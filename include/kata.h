@@ -442,7 +442,8 @@ kata_status kata_decode_step_packed(const void *q, const void *k, const void *v,
  * dq and dk must not overlap any input.
  *
  * Weights, inv_freq: 16-byte aligned like every pointer (positions: 8); B * T *
- * (Hq + Hk) at most 2^40, B and T below 2^31 - 2^17, else KATA_ERR_UNSUPPORTED.
+ * (Hq + Hk) at most 2^40, B, T, Hq and Hk below 2^31 - 2^17, else
+ * KATA_ERR_UNSUPPORTED.
  * Offsets are 64-bit.
  */
 kata_status kata_qk_norm_rotate(const void *q, const void *k, void *q_out, void *k_out,

@@ -21,8 +21,10 @@ kata_status norm_sizes(int B, int T, int Hq, int Hk, int d, kata_dtype dtype, No
     if (B < 1 || T < 1 || Hq < 1 || Hk < 0 || d < 1) return KATA_ERR_INVALID_ARG;
     if (dtype != KATA_F32 && dtype != KATA_BF16) return KATA_ERR_UNSUPPORTED;
     if (d != 16 && d != 32 && d != 64) return KATA_ERR_UNSUPPORTED;
-    // a warp's step past the last token fits
-    if (B > 0x7fffffff - (1 << 17) || T > 0x7fffffff - (1 << 17)) return KATA_ERR_UNSUPPORTED;
+    // a warp's step past the last token, and a block row's past the last head (of at most 444
+    // block rows of 64 heads), fit
+    const int most = 0x7fffffff - (1 << 17);
+    if (B > most || T > most || Hq > most || Hk > most) return KATA_ERR_UNSUPPORTED;
     if ((long long)B * T > (1LL << 40) / ((long long)Hq + Hk)) return KATA_ERR_UNSUPPORTED;
     p.B = B;
     p.T = T;

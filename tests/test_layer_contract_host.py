@@ -6,7 +6,7 @@ import random
 
 import pytest
 
-from tests.test_layer_abi_host import INV, WS, at, lib, norm_bwd  # noqa: F401  (lib: a fixture)
+from tests.test_layer_abi_host import INV, UNS, WS, at, lib, norm, norm_bwd  # noqa: F401  (lib: a fixture)
 
 
 # ------------------------------------------------------- dq and dk in one buffer
@@ -69,3 +69,19 @@ def test_a_layout_is_taken_only_without_a_shared_element(lib):
             taken += 1
             assert not rows_meet(n, dq, dk, gap, H, 16), (n, H, dq, dk, gap)
     assert taken > 500
+
+
+# ------------------------------------------------------------------ head counts
+
+def test_head_counts_near_2_to_31_are_refused(lib):
+    # the set counts of a block row would pass 2^31
+    W = lib.kata_qk_norm_rotate_backward_workspace_bytes
+    top = 2 ** 31 - 2 ** 17
+    for d in (16, 32, 64):
+        assert W(1, 1, top - 1, 1, d) > 0 and W(1, 1, 1, top - 1, d) > 0
+        for n in (top, 2 ** 31 - 64, 2 ** 31 - 1):
+            assert W(1, 1, n, 1, d) == 0 and W(1, 1, 1, n, d) == 0
+    far = dict(B=1, T=1, qs=(0, 0, 64), ks=(0, 0, 64), dqs=(0, 0, 64), dks=(0, 0, 64))
+    for bad in (dict(Hq=top), dict(Hk=top), dict(Hq=2 ** 31 - 1), dict(Hk=2 ** 31 - 1)):
+        assert norm(lib, **{k: x for k, x in far.items() if k[0] != "d"}, **bad) == UNS
+        assert norm_bwd(lib, **far, **bad) == UNS
