@@ -13,8 +13,7 @@ namespace {
 // Row statistics of the backward pass: delta = -dy.y (y the forward's unrounded
 // output) and 1 / den (0 for a row without weight), zeros in the padding up to
 // R_pad.
-__device__ __forceinline__ float dot8(const float *a, const float4 &x, const float4 &y) {
-    const float4 u = *reinterpret_cast<const float4 *>(a), v = *reinterpret_cast<const float4 *>(a + 4);
+__device__ __forceinline__ float dot8(const float4 &u, const float4 &v, const float4 &x, const float4 &y) {
     float s = u.x * x.x;
     s = fmaf(u.y, x.y, s);
     s = fmaf(u.z, x.z, s);
@@ -24,13 +23,17 @@ __device__ __forceinline__ float dot8(const float *a, const float4 &x, const flo
     s = fmaf(v.z, y.z, s);
     return fmaf(v.w, y.w, s);
 }
+__device__ __forceinline__ float dot8(const float *a, const float4 &x, const float4 &y) {
+    const float4 *u = reinterpret_cast<const float4 *>(a);
+    return dot8(u[0], u[1], x, y);
+}
 __device__ __forceinline__ float dot8(const __nv_bfloat16 *a, const float4 &x, const float4 &y) {
     const uint4 w = *reinterpret_cast<const uint4 *>(a);
-    const float u[8] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                        __uint_as_float(w.y & 0xFFFF0000u), __uint_as_float(w.z << 16),
-                        __uint_as_float(w.z & 0xFFFF0000u), __uint_as_float(w.w << 16),
-                        __uint_as_float(w.w & 0xFFFF0000u)};
-    return dot8(u, x, y);
+    const float4 u = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                                 __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+    const float4 v = make_float4(__uint_as_float(w.z << 16), __uint_as_float(w.z & 0xFFFF0000u),
+                                 __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xFFFF0000u));
+    return dot8(u, v, x, y);
 }
 
 template <typename T>

@@ -115,7 +115,8 @@ cross_few_kernel(const FArgs a) {
     constexpr int N = kXCols / (kFWarps * KW);      // key groups of a warp per block
     constexpr int U = N < 4 ? N : 4;                // of them in flight
     __shared__ XRange range;
-    __shared__ float red[kFWarps][RB][D], red_l[kFWarps][RB];
+    __shared__ __align__(16) float red[kFWarps][RB][D];
+    __shared__ float red_l[kFWarps][RB];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, key = lane / L, c = 8 * (lane % L);
     few_begin<T, D>(a, range);
     const int rows = a.sched.rows;
@@ -258,7 +259,8 @@ cross_rows_kernel(const FArgs a) {
     constexpr int W = D / 8;  // words of a lane: D / 4 coordinates
     static_assert(kXCols == 16 * kFWarps, "a warp takes 16 keys of a block");
     __shared__ XRange range;
-    __shared__ float red[kFWarps][16][D], red_l[kFWarps][16];
+    __shared__ __align__(16) float red[kFWarps][16][D];
+    __shared__ float red_l[kFWarps][16];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = (lane % 4) * (D / 4);
     few_begin<T, D>(a, range);
     const int rows = a.sched.rows;

@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(32 * kNormWarps, norm_per_sm(BWD))
 norm_rotate_kernel(const NormArgs<T> a) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes, U = norm_groups(BWD, sizeof(T));
     using Row = Row8<T, INTER>;
-    __shared__ float2 cs_buf[kNormWarps][32];
+    __shared__ __align__(16) float2 cs_buf[kNormWarps][32];
     __shared__ float w_buf[2][D];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, sub = lane / kLanes;
     const Lane<D, INTER> L(lane, a.n_rot);

@@ -1,11 +1,15 @@
 """Host-side promises of the head norm's and cross attention's entry points (no GPU).  As
 in tests/test_layer_abi_host.py every call passes fake addresses and is refused; what an
 accepted call is refused for, last of all, is its missing workspace (WS)."""
+import glob
 import itertools
+import os
 import random
+import re
 
 import pytest
 
+from kernelized_linear_attention_fwd_b200.csrc import build as kbuild
 from tests.test_layer_abi_host import INV, UNS, WS, at, lib, norm, norm_bwd  # noqa: F401  (lib: a fixture)
 
 
@@ -85,3 +89,34 @@ def test_head_counts_near_2_to_31_are_refused(lib):
     for bad in (dict(Hq=top), dict(Hk=top), dict(Hq=2 ** 31 - 1), dict(Hk=2 ** 31 - 1)):
         assert norm(lib, **{k: x for k, x in far.items() if k[0] != "d"}, **bad) == UNS
         assert norm_bwd(lib, **far, **bad) == UNS
+
+
+# ---------------------------------------------------------- alignment of arrays
+
+SIZES = {"float": 4, "int": 4, "uint32_t": 4, "uint16_t": 2, "uint8_t": 1, "float2": 8, "uint2": 8, "uint64_t": 8,
+         "float4": 16, "uint4": 16}
+ARRAY = re.compile(r"(__shared__\s+)?(?:alignas|__align__)?(\(\d+\))?\s*\b(%s)\s+([^;=()]*\[[^;=()]*)[;=]" % "|".join(SIZES))
+CAST = re.compile(r"reinterpret_cast<(?:const )?(float2|uint2|uint64_t|float4|uint4) \*>\(&?(\w+)\b")
+
+
+def under_aligned(source):
+    """Names of arrays that are read or written as vectors wider than they are aligned, function by
+    function (a function opens at a line that starts with a brace's head and ends at `}` in column 0)."""
+    found = []
+    for body in re.split(r"(?m)^\}", source):
+        align = {}
+        for m in ARRAY.finditer(body):
+            a = int(m.group(2)[1:-1]) if m.group(2) else SIZES[m.group(3)]
+            for name in re.findall(r"(\w+)(?:\[[^\]]*\])+", m.group(4)):
+                align[name] = a
+        found += [m.group(2) for m in CAST.finditer(body) if align.get(m.group(2), 16) < SIZES[m.group(1)]]
+    return found
+
+
+def test_arrays_read_as_vectors_are_aligned_for_it():
+    bad = "__global__ void f() {\n    __shared__ float a[4][8], b[2];\n    *reinterpret_cast<float4 *>(&a[i][4]) = x;\n}\n"
+    assert under_aligned(bad) == ["a"]
+    assert under_aligned(bad.replace("float a[", "__align__(16) float a[")) == []
+    for path in sorted(glob.glob(os.path.join(kbuild.HERE, "*.cu*"))):
+        with open(path) as f:
+            assert under_aligned(f.read()) == [], os.path.basename(path)
