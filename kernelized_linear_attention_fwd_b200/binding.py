@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkata.so")
@@ -132,17 +133,21 @@ def load_library(path: str = LIB_PATH):
     lib.kata_get_device_status.restype = i32
     lib.kata_get_device_status.argtypes = [vp]
     _lib = lib
-    _bind_calls(lib)
+    if "torch" in sys.modules:
+        _bind_calls(lib)
     return lib
 
 
 # The short cut of the short calls (csrc/torch_calls.cpp), or None: every call below
-# that takes it also works without it, through the same C functions.
+# that takes it also works without it, through the same C functions.  Looked for once
+# torch is loaded: loading the library for host buffers or sizes does not load torch.
 _calls = None
+_calls_sought = False
 
 
 def _bind_calls(lib):
-    global _calls
+    global _calls, _calls_sought
+    _calls_sought = True
     path = os.path.join(_HERE, "_calls.so")
     if not os.path.exists(path):
         return
@@ -166,8 +171,8 @@ def _bind_calls(lib):
 
 def _short(name, *args):
     """The short cut's outputs, or NotImplemented where it does not take the call."""
-    if _lib is None:
-        load_library()
+    if not _calls_sought and "torch" in sys.modules:
+        _bind_calls(load_library())
     if _calls is None:
         return NotImplemented
     r = getattr(_calls, name)(*args)
