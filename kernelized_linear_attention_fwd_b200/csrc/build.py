@@ -4,12 +4,13 @@
 
 The shared object lands in the package directory beside the Python binding.
 Beside it lands _calls.so, the binding's short cut (torch_calls.cpp, g++ against
-torch's headers); without those headers it is left out and the binding works
-without it.  Cross-compiles without a GPU.  `--verbose` adds -Xptxas -v (registers, spills,
+torch's headers); where torch, a header or the compiler is missing, or the compiler
+fails, it is left out and the binding works without it.  Cross-compiles without a GPU.  `--verbose` adds -Xptxas -v (registers, spills,
 shared memory per kernel).
 """
 import glob
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -46,18 +47,29 @@ def up_to_date():
     return all(os.path.getmtime(f) <= t for f in sources() + headers() + [__file__])
 
 
-def calls_command(out):
-    """The g++ command of _calls.so, or None where a header it needs is missing."""
-    import torch
+def cuda_include():
+    """The CUDA toolkit's headers: of CUDA_HOME, of the compiler in use, or in the usual place."""
+    nvcc = shutil.which(os.environ.get("NVCC", "nvcc"))
+    homes = [os.environ.get("CUDA_HOME"), os.environ.get("CUDA_PATH"),
+             nvcc and os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "/usr/local/cuda"]
+    found = [d for d in (os.path.join(h, "include") for h in homes if h)
+             if os.path.exists(os.path.join(d, "cuda_runtime_api.h"))]
+    return found[0] if found else None
 
+
+def calls_command(out):
+    """The g++ command of _calls.so, or None where torch or a header it needs is missing."""
+    try:
+        import torch
+    except ImportError:
+        return None
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
-    dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"),
-            sysconfig.get_paths()["include"], "/usr/local/cuda/include"]
-    needed = [os.path.join(inc, "ATen", "ATen.h"), os.path.join(dirs[2], "Python.h"),
-              os.path.join(dirs[3], "cuda_runtime_api.h")]
-    if not all(os.path.exists(f) for f in needed):
+    python, cuda = sysconfig.get_paths()["include"], cuda_include()
+    needed = [os.path.join(inc, "ATen", "ATen.h"), os.path.join(python, "Python.h")]
+    if cuda is None or not all(os.path.exists(f) for f in needed):
         return None
+    dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), python, cuda]
     return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", CALLS_SRC, "-o", out]
             + ["-I" + d for d in dirs]
             + ["-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib])
@@ -65,35 +77,47 @@ def calls_command(out):
 
 def build_calls(force=False):
     """Starts building _calls.so if it is missing or older than its sources; returns a
-    function that waits for it."""
+    function that waits for it.  Where it cannot be built it is left out, an older one too,
+    which was built for other declarations."""
     deps = [CALLS_SRC, os.path.join(ROOT, "include", "kata.h"), __file__]
     if (not force and os.path.exists(CALLS_OUT)
             and all(os.path.getmtime(f) <= os.path.getmtime(CALLS_OUT) for f in deps)):
         return lambda: None
+
+    def without(why):
+        print(why + ": built without _calls.so")
+        if os.path.exists(CALLS_OUT):
+            os.remove(CALLS_OUT)
+
     tmp = CALLS_OUT + ".tmp%d" % os.getpid()
     cmd = calls_command(tmp)
     if cmd is None:
-        print("torch or Python headers not found: built without _calls.so")
-        return lambda: None
-    proc = subprocess.Popen(cmd)
+        return lambda: without("torch or headers not found")
+    try:
+        proc = subprocess.Popen(cmd)
+    except OSError:
+        return lambda: without(cmd[0] + " not found")
 
     def finish():
-        if proc.wait() != 0:
-            raise subprocess.CalledProcessError(proc.returncode, cmd)
-        os.replace(tmp, CALLS_OUT)
+        if proc.wait() == 0:
+            os.replace(tmp, CALLS_OUT)
+        else:
+            without("%s failed (%d)" % (cmd[0], proc.returncode))
 
     return finish
 
 
 def build(force=False, verbose=False):
     finish = build_calls(force)
-    if force or verbose or not up_to_date():
-        nvcc = os.environ.get("NVCC", "nvcc")
-        tmp = OUT + ".tmp%d" % os.getpid()
-        cmd = [nvcc] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose else []) + sources() + ["-o", tmp]
-        subprocess.check_call(cmd)
-        os.replace(tmp, OUT)
-    finish()
+    try:
+        if force or verbose or not up_to_date():
+            nvcc = os.environ.get("NVCC", "nvcc")
+            tmp = OUT + ".tmp%d" % os.getpid()
+            cmd = [nvcc] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose else []) + sources() + ["-o", tmp]
+            subprocess.check_call(cmd)
+            os.replace(tmp, OUT)
+    finally:
+        finish()
     return OUT
 
 

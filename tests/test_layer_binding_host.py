@@ -38,3 +38,67 @@ def test_the_short_cut_is_found_by_the_first_call_with_tensors():
                "except K.KataError: pass\n"
                "assert binding._calls is not None")
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.fixture
+def elsewhere(tmp_path, monkeypatch):
+    """The build's outputs in an empty folder, and nvcc replaced by a copy of nothing."""
+    monkeypatch.setattr(kbuild, "OUT", str(tmp_path / "libkata.so"))
+    monkeypatch.setattr(kbuild, "CALLS_OUT", str(tmp_path / "_calls.so"))
+    ran = []
+
+    def check_call(cmd):
+        ran.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    monkeypatch.setattr(kbuild.subprocess, "check_call", check_call)
+    return tmp_path, ran
+
+
+def names(folder):
+    return sorted(p.name for p in folder.iterdir())
+
+
+def test_the_library_is_built_without_torch(elsewhere, monkeypatch):
+    folder, ran = elsewhere
+    (folder / "_calls.so").write_text("of an earlier build")
+    monkeypatch.setitem(sys.modules, "torch", None)  # import torch fails
+    assert kbuild.build(force=True) == str(folder / "libkata.so")
+    assert len(ran) == 1 and names(folder) == ["libkata.so"]
+
+
+@pytest.mark.parametrize("cmd", [["false"], ["/no/such/compiler"]])
+def test_the_library_is_built_where_the_short_cut_fails(elsewhere, monkeypatch, cmd):
+    folder, ran = elsewhere
+    (folder / "_calls.so").write_text("of an earlier build")
+    monkeypatch.setattr(kbuild, "calls_command", lambda out: cmd)
+    kbuild.build(force=True)
+    assert len(ran) == 1 and names(folder) == ["libkata.so"]
+
+
+def test_a_failing_library_build_leaves_no_compiler_behind(elsewhere, monkeypatch):
+    folder, _ = elsewhere
+    monkeypatch.setattr(kbuild, "calls_command", lambda out: ["sh", "-c", "sleep 0.3; : > " + out])
+
+    def fails(cmd):
+        raise subprocess.CalledProcessError(1, cmd)
+
+    monkeypatch.setattr(kbuild.subprocess, "check_call", fails)
+    with pytest.raises(subprocess.CalledProcessError):
+        kbuild.build(force=True)
+    assert names(folder) == ["_calls.so"]  # waited for
+
+
+def test_headers_are_those_of_the_toolkit_in_use(tmp_path, monkeypatch):
+    (tmp_path / "include").mkdir()
+    (tmp_path / "include" / "cuda_runtime_api.h").write_text("")
+    (tmp_path / "bin").mkdir()
+    nvcc = tmp_path / "bin" / "nvcc"
+    nvcc.write_text("#!/bin/sh")
+    nvcc.chmod(0o755)
+    for name in ("CUDA_HOME", "CUDA_PATH"):
+        monkeypatch.delenv(name, raising=False)
+    monkeypatch.setenv("NVCC", str(nvcc))
+    assert kbuild.cuda_include() == str(tmp_path / "include")
+    monkeypatch.setenv("CUDA_HOME", "/no/such/place")
+    assert kbuild.cuda_include() == str(tmp_path / "include")
