@@ -145,21 +145,29 @@ _calls = None
 _calls_sought = False
 
 
+def calls_file():
+    """Name of the short cut for the running Python and torch.  It reads tensors by torch's
+    C++ layout, so one that was built for others is never loaded, whether or not it would load."""
+    import importlib.machinery
+
+    import torch
+
+    return f"_calls-torch{torch.__version__}{importlib.machinery.EXTENSION_SUFFIXES[0]}"
+
+
 def _bind_calls(lib):
     global _calls, _calls_sought
     _calls_sought = True
-    path = os.path.join(_HERE, "_calls.so")
+    path = os.path.join(_HERE, calls_file())
     if not os.path.exists(path):
         return
     import importlib.util
 
     try:
-        import torch  # noqa: F401  (loads its libraries)
-
         spec = importlib.util.spec_from_file_location("_calls", path)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
-    except ImportError:  # built against another torch or Python
+    except ImportError:  # a library that it needs is gone
         return
     mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.kata_qk_norm_rotate, lib.kata_qk_norm_rotate_backward,

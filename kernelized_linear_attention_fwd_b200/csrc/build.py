@@ -3,12 +3,14 @@
     python kernelized_linear_attention_fwd_b200/csrc/build.py [--verbose]
 
 The shared object lands in the package directory beside the Python binding.
-Beside it lands _calls.so, the binding's short cut (torch_calls.cpp, g++ against
-torch's headers); where torch, a header or the compiler is missing, or the compiler
-fails, it is left out and the binding works without it.  Cross-compiles without a GPU.  `--verbose` adds -Xptxas -v (registers, spills,
-shared memory per kernel).
+Beside it lands _calls-torch<version>.<Python's suffix>.so, the binding's short cut
+(torch_calls.cpp, g++ against torch's headers); where torch, a header or the compiler is
+missing, or the compiler fails, it is left out and the binding works without it.
+Cross-compiles without a GPU.  `--verbose` adds -Xptxas -v (registers, spills, shared
+memory per kernel).
 """
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -21,7 +23,6 @@ ROOT = os.path.dirname(PKG)
 OUT = os.path.join(PKG, "libkata.so")
 
 CALLS_SRC = os.path.join(HERE, "torch_calls.cpp")
-CALLS_OUT = os.path.join(PKG, "_calls.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -57,12 +58,22 @@ def cuda_include():
     return found[0] if found else None
 
 
-def calls_command(out):
-    """The g++ command of _calls.so, or None where torch or a header it needs is missing."""
+def calls_out():
+    """Where the short cut for the running Python and torch lies, or None without torch."""
     try:
-        import torch
+        import torch  # noqa: F401
     except ImportError:
         return None
+    spec = importlib.util.spec_from_file_location("binding", os.path.join(HERE, "..", "binding.py"))
+    binding = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(binding)
+    return os.path.join(PKG, binding.calls_file())
+
+
+def calls_command(out):
+    """The g++ command of the short cut, or None where a header it needs is missing."""
+    import torch
+
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     python, cuda = sysconfig.get_paths()["include"], cuda_include()
@@ -76,21 +87,24 @@ def calls_command(out):
 
 
 def build_calls(force=False):
-    """Starts building _calls.so if it is missing or older than its sources; returns a
-    function that waits for it.  Where it cannot be built it is left out, an older one too,
-    which was built for other declarations."""
+    """Starts building the short cut if it is missing or older than its sources; returns a
+    function that waits for it.  Where it cannot be built it is left out.  Older ones, which were
+    built for other declarations, are removed, whatever torch and Python they are for."""
     deps = [CALLS_SRC, os.path.join(ROOT, "include", "kata.h"), __file__]
-    if (not force and os.path.exists(CALLS_OUT)
-            and all(os.path.getmtime(f) <= os.path.getmtime(CALLS_OUT) for f in deps)):
+    for f in glob.glob(os.path.join(PKG, "_calls*.so")):
+        if any(os.path.getmtime(d) > os.path.getmtime(f) for d in deps):
+            os.remove(f)
+    out = calls_out()
+    if out and os.path.exists(out) and not force:
         return lambda: None
 
     def without(why):
-        print(why + ": built without _calls.so")
-        if os.path.exists(CALLS_OUT):
-            os.remove(CALLS_OUT)
+        print(why + ": built without " + os.path.basename(out or "_calls.so"))
+        if out and os.path.exists(out):
+            os.remove(out)
 
-    tmp = CALLS_OUT + ".tmp%d" % os.getpid()
-    cmd = calls_command(tmp)
+    tmp = "%s.tmp%d" % (out, os.getpid())
+    cmd = calls_command(tmp) if out else None
     if cmd is None:
         return lambda: without("torch or headers not found")
     try:
@@ -100,7 +114,7 @@ def build_calls(force=False):
 
     def finish():
         if proc.wait() == 0:
-            os.replace(tmp, CALLS_OUT)
+            os.replace(tmp, out)
         else:
             without("%s failed (%d)" % (cmd[0], proc.returncode))
 

@@ -1,10 +1,12 @@
 """The binding's short cut (csrc/torch_calls.cpp): when it is loaded and how it is built (no GPU)."""
 import os
+import shutil
 import subprocess
 import sys
 
 import pytest
 
+from kernelized_linear_attention_fwd_b200 import binding
 from kernelized_linear_attention_fwd_b200.csrc import build as kbuild
 
 ROOT = kbuild.ROOT
@@ -44,7 +46,7 @@ def test_the_short_cut_is_found_by_the_first_call_with_tensors():
 def elsewhere(tmp_path, monkeypatch):
     """The build's outputs in an empty folder, and nvcc replaced by a copy of nothing."""
     monkeypatch.setattr(kbuild, "OUT", str(tmp_path / "libkata.so"))
-    monkeypatch.setattr(kbuild, "CALLS_OUT", str(tmp_path / "_calls.so"))
+    monkeypatch.setattr(kbuild, "PKG", str(tmp_path))
     ran = []
 
     def check_call(cmd):
@@ -59,9 +61,16 @@ def names(folder):
     return sorted(p.name for p in folder.iterdir())
 
 
+def earlier(folder):
+    """Short cuts of other Pythons and torches, older than their sources."""
+    for name in ("_calls.so", "_calls-torch1.0.cpython-38-x86_64-linux-gnu.so", binding.calls_file()):
+        (folder / name).write_text("")
+        os.utime(folder / name, (1, 1))
+
+
 def test_the_library_is_built_without_torch(elsewhere, monkeypatch):
     folder, ran = elsewhere
-    (folder / "_calls.so").write_text("of an earlier build")
+    earlier(folder)
     monkeypatch.setitem(sys.modules, "torch", None)  # import torch fails
     assert kbuild.build(force=True) == str(folder / "libkata.so")
     assert len(ran) == 1 and names(folder) == ["libkata.so"]
@@ -70,7 +79,8 @@ def test_the_library_is_built_without_torch(elsewhere, monkeypatch):
 @pytest.mark.parametrize("cmd", [["false"], ["/no/such/compiler"]])
 def test_the_library_is_built_where_the_short_cut_fails(elsewhere, monkeypatch, cmd):
     folder, ran = elsewhere
-    (folder / "_calls.so").write_text("of an earlier build")
+    earlier(folder)
+    (folder / binding.calls_file()).write_text("of a build just now")
     monkeypatch.setattr(kbuild, "calls_command", lambda out: cmd)
     kbuild.build(force=True)
     assert len(ran) == 1 and names(folder) == ["libkata.so"]
@@ -86,7 +96,7 @@ def test_a_failing_library_build_leaves_no_compiler_behind(elsewhere, monkeypatc
     monkeypatch.setattr(kbuild.subprocess, "check_call", fails)
     with pytest.raises(subprocess.CalledProcessError):
         kbuild.build(force=True)
-    assert names(folder) == ["_calls.so"]  # waited for
+    assert names(folder) == [binding.calls_file()]  # waited for
 
 
 def test_headers_are_those_of_the_toolkit_in_use(tmp_path, monkeypatch):
@@ -102,3 +112,28 @@ def test_headers_are_those_of_the_toolkit_in_use(tmp_path, monkeypatch):
     assert kbuild.cuda_include() == str(tmp_path / "include")
     monkeypatch.setenv("CUDA_HOME", "/no/such/place")
     assert kbuild.cuda_include() == str(tmp_path / "include")
+
+
+def test_the_short_cut_of_another_torch_or_python_is_not_loaded(tmp_path, monkeypatch):
+    import importlib.machinery
+
+    import torch
+
+    lib, mine = binding.load_library(), binding.calls_file()
+    shutil.copy(os.path.join(kbuild.PKG, mine), tmp_path / mine)
+    monkeypatch.setattr(binding, "_HERE", str(tmp_path))
+    for where, name, value in ((torch, "__version__", torch.__version__ + ".1"),
+                               (importlib.machinery, "EXTENSION_SUFFIXES", [".cpython-399-x86_64-linux-gnu.so"])):
+        with monkeypatch.context() as m:
+            m.setattr(binding, "_calls", None)
+            m.setattr(where, name, value)
+            binding._bind_calls(lib)
+            assert binding._calls is None and binding.calls_file() != mine
+            # nor under the name of a build that recorded nothing
+            shutil.copy(tmp_path / mine, tmp_path / "_calls.so")
+            binding._bind_calls(lib)
+            assert binding._calls is None
+    with monkeypatch.context() as m:
+        m.setattr(binding, "_calls", None)
+        binding._bind_calls(lib)
+        assert binding._calls is not None
