@@ -470,7 +470,9 @@ kata_status kata_qk_norm_rotate_backward(
  *     y_t  = sum_{s < key_lengths[b]} w_ts v_s / l_t              (0 if l_t = 0)
  *
  * (the weights of this file's head with the causal mask replaced by a length;
- * the convex output gate of summary 2.1 holds as before).
+ * the convex output gate of summary 2.1 holds as before).  Weights and their
+ * sums are fp32 numbers: l_t below 2^-126, the smallest normal one, counts as 0
+ * (here and in the gradient), and past 2^128 y_t is not a number.
  *
  *   q      [B, H, Tq, d] dtype     out  [B, H, Tq, d] dtype
  *   k, v   [B, Hkv, Tk, d] dtype; Hkv divides H, query head h uses key head

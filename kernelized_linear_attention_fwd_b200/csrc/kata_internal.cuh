@@ -292,8 +292,10 @@ constexpr int kF32Tile = 64;
 __device__ __forceinline__ int cross_length(const int *key_lengths, int b, int Tk) {
     return key_lengths ? min(max(__ldg(key_lengths + b), 0), Tk) : Tk;
 }
-// 1 / den, and 0 for a row without weight.
-__device__ __forceinline__ float cross_recip(float den) { return den == 0.f ? 0.f : 1.f / den; }
+// 1 / den, and 0 for a row without weight.  Sums below the smallest normal number count as
+// none: their reciprocals overflow, and one such query would make every key's gradient
+// infinite or NaN.
+__device__ __forceinline__ float cross_recip(float den) { return den < 1.17549435e-38f ? 0.f : 1.f / den; }
 
 // Decode step on the dense (d^2 rows) or packed (d(d+1)/2 rows) state layout.
 cudaError_t launch_decode(int B, int H, int dk, int dv, kata_dtype dtype, const void *q,

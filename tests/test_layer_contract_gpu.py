@@ -79,3 +79,24 @@ def test_gradients_of_padded_keys_are_zero_whatever_the_queries_hold(dtype, Tq, 
                 assert not dk[b, :, int(n[b]):].any() and not dv[b, :, int(n[b]):].any(), (d, bad, b)
                 # key head 1 has none of the bad row
                 assert bool(torch.isfinite(dk[b, 1]).all()) and bool(torch.isfinite(dv[b, 1]).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,Tq,Tk", [(2, 200, 300), (2, 1, 300), (8, 1, 5000), (2, 40, 100), (2, 3, 9000)])
+def test_weights_below_the_normal_numbers_count_as_none(dtype, H, Tq, Tk):
+    # s about 2^-72, l below 2^-126 though not 0 in fp32: zeros, as of a query without weight,
+    # and nothing of that query in the keys' gradients
+    q, k, v, g = make(2, H, 2, Tq, Tk, 64, dtype, seed=Tk)
+    tiny, none = q.clone(), q.clone()
+    tiny[:, :, Tq // 2] *= 2.0 ** -75
+    none[:, :, Tq // 2] = 0
+    for n in (None, lens(Tk, Tk // 2)):
+        out, y, den = forward(tiny, k, v, n)
+        assert not out[:, :, Tq // 2].any() and not y[:, :, Tq // 2].any()
+        assert float(den[:, :, Tq // 2].max()) < 2.0 ** -126
+        assert not K.kata_cross_forward(tiny, k, v, key_lengths=n)[:, :, Tq // 2].any()
+        grads = K.kata_cross_backward(g, tiny, k, v, y, den, key_lengths=n)
+        o0, y0, den0 = forward(none, k, v, n)
+        assert torch.equal(out, o0)
+        for a, b in zip(grads, K.kata_cross_backward(g, none, k, v, y0, den0, key_lengths=n)):
+            assert torch.equal(a, b)
