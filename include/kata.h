@@ -489,8 +489,10 @@ kata_status kata_qk_norm_rotate_backward(
  *
  * KATA_BF16 runs on the tensor cores for every d (fp32 accumulation; the weights
  * are rounded to bf16 once, in the numerator and the denominator alike; with y_out
- * and heads or keys few enough for that to show in a gradient, to a sum of two bf16
- * numbers, and so in kata_cross_backward).  KATA_F32
+ * and heads or keys few enough for that to show in a gradient (d of 16 or 32, or at
+ * most 256 keys), to a sum of two bf16 numbers, and so in kata_cross_backward).  So
+ * the last bit of out may differ with and without y_out: give it to every call whose
+ * bits have to repeat, and to one whose weights need 16 bits at these sizes.  KATA_F32
  * keeps fp32 accuracy: its products are sums of products of three bf16 numbers per
  * operand (24 bits; for magnitudes between 2^-100 and 2^127, and not-a-number where
  * an infinity is visible).  At most 2 rows per key head ((H / Hkv) * Tq, a decode step),

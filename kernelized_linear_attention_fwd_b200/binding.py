@@ -5,6 +5,10 @@ the library's CUDA kernels.  Tensors are torch CUDA tensors (torch supplies
 device memory and streams); the functions carry the C names and raise
 ``KataError`` on any status other than KATA_OK.  There is no fallback: if
 libkata.so is missing or fails to load, every call raises.
+
+No call records an autograd graph, whether or not its inputs require gradients: its
+outputs do not.  Where a call has a gradient (kata_qk_norm_rotate_backward,
+kata_cross_backward), wrap the two in a torch.autograd.Function.
 """
 from __future__ import annotations
 
@@ -829,7 +833,7 @@ def kata_qk_norm_rotate(q, k=None, q_weight=None, k_weight=None, inv_freq=None, 
     projection), times the fp32 gains q_weight, k_weight [d] (None: 1), rotated
     by position * inv_freq [n_rot] fp32 (None: no rotation).  positions: int64
     [B,T] or [T] (None: 0 .. T-1).  interleaved: pairs (2i, 2i+1) instead of
-    (i, i + n_rot)."""
+    (i, i + n_rot).  No autograd graph."""
     if stream is None:
         r = _short("qk_norm_rotate", q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved,
                    q_out, k_out)
@@ -956,7 +960,9 @@ def kata_cross_forward(q, k, v, key_lengths=None, out=None, y_out=None, den_out=
     (int32 [B]; None: all) of the keys k, v [B,Hkv,Tk,d] of another sequence;
     Hkv divides H.  Rows without weight are zero.  y_out [B,H,Tq,d] and den_out
     [B,H,Tq] (optional, fp32) receive the unrounded output and the summed
-    weights, which kata_cross_backward reads."""
+    weights, which kata_cross_backward reads.  With y_out the weights of a bf16 call
+    may keep more bits (heads of 16 and 32, up to 256 keys), so the output's last bit may
+    differ: give it to every call whose bits have to repeat.  No autograd graph."""
     import torch
 
     if stream is None:
@@ -988,7 +994,8 @@ def kata_cross_backward_workspace_bytes(B, H, Hkv, Tq, Tk, d, dtype_code) -> int
 def kata_cross_backward(dout, q, k, v, y, den, key_lengths=None, dq=None, dk=None, dv=None,
                         workspace=None, stream=None):
     """(dq, dk, dv): the gradient of kata_cross_forward, from that of its output
-    and what it wrote to y_out and den_out for the same q, k, v, key_lengths."""
+    and what it wrote to y_out and den_out for the same q, k, v, key_lengths (for an
+    autograd.Function to return: the forward records no graph)."""
     import torch
 
     if stream is None:

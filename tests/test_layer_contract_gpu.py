@@ -5,6 +5,8 @@ from __future__ import annotations
 
 import pytest
 
+from tests import layer_oracle as O
+
 pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
@@ -100,3 +102,32 @@ def test_weights_below_the_normal_numbers_count_as_none(dtype, H, Tq, Tk):
         assert torch.equal(out, o0)
         for a, b in zip(grads, K.kata_cross_backward(g, none, k, v, y0, den0, key_lengths=n)):
             assert torch.equal(a, b)
+
+
+def test_a_pair_of_calls_in_an_autograd_function():
+    # as the README has it
+    class Cross(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, v, lengths):
+            y = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+            den = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+            out = K.kata_cross_forward(q, k, v, key_lengths=lengths, y_out=y, den_out=den)
+            ctx.save_for_backward(q, k, v, y, den, lengths)
+            return out
+
+        @staticmethod
+        def backward(ctx, g):
+            *saved, lengths = ctx.saved_tensors
+            return (*K.kata_cross_backward(g.contiguous(), *saved, key_lengths=lengths), None)
+
+    q, k, v, g = (t.requires_grad_() for t in make(2, 4, 2, 33, 70, 32, "f32", seed=21))
+    assert not K.kata_cross_forward(q, k, v).requires_grad  # the call itself records nothing
+    g = g.detach()
+    for n in (None, lens(70, 11)):
+        for up, loss in ((g, lambda t: (t * g).sum()), (torch.ones_like(g), lambda t: t.sum())):
+            # the gradients of two uses add up
+            got = torch.autograd.grad(loss(Cross.apply(q, k, v, n)) + loss(Cross.apply(q, k, v, n)), (q, k, v))
+            ref = O.cross_grad(up, q.detach(), k.detach(), v.detach(), n)
+            bounds = O.cross_bounds(q.detach(), k.detach(), v.detach(), torch.float32, n, dout=up)
+            for a, r, b in zip(got, ref, bounds):
+                assert O.worst(a / 2, r, b) <= 1
