@@ -1,5 +1,7 @@
 // Cross attention with KATA weights in fp32 (formulas and modes: cross_tc.cu), on the
-// tensor cores with every fp32 operand as the sum of three bf16 numbers:
+// tensor cores with every fp32 operand as the sum of three bf16 numbers (the published
+// splitting of Henry, Tang and Heinecke, "Leveraging the bfloat16 Artificial Intelligence
+// Datatype For Higher-Precision Computations", ARITH 2019):
 //
 //   x = h + m + l,  h = bf16(x), m = bf16(x - h), l = bf16(x - h - m)
 //
@@ -19,11 +21,13 @@
 // The register-level products (mma.sync) suit tiles this small, whose split takes
 // the arithmetic of all the warps: tcgen05 would need the three planes of the
 // weights in tensor memory beside their scores, 192 columns where a step of the bf16
-// kernel has 128.  Measured (8 heads, 2048 queries and keys, d = 64): forward 159 us,
-// gradient 485 us, which is 54 and 62 TFLOP/s of fp32 products (the CUDA cores' form of
-// this kernel: 279 and 915 us, bound by its shared-memory reads); bound by the
-// register-level products, whose pipe is 66 to 74% active.  (With twice as many chains of
-// products side by side: the same.)
+// kernel has 128.  Measured (8 heads, 2048 queries and keys, d = 64): forward 153 us,
+// gradient 475 us, which is 56 and 63 TFLOP/s of fp32 products (the CUDA cores' form of
+// this kernel: 279 and 915 us, bound by its shared-memory reads; 8192 queries and keys:
+// 2.02 and 6.7 ms, 68 and 72 TFLOP/s).  The register-level products' pipe is 66 to 74%
+// active; six products at the bf16 rate of tcgen05 would allow some 275 TFLOP/s, so this
+// path is a choice of simplicity for a precision that serves small training, not a limit.
+// (With twice as many chains of products side by side: the same.)
 #include <cuda_bf16.h>
 
 #include "kata_internal.cuh"

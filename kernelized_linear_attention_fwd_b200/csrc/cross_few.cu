@@ -5,7 +5,8 @@
 // Bound by reading the keys and values once.  64 sequences of 1501 keys and less, 16
 // heads, one query (270 MB): 45 us, 6.0 TB/s, against 60 us on the tensor cores, whose
 // one group of warps per item takes longer over 128 rows of scores than their
-// block's loads.  Past 4 rows the registers of the rows' accumulators crowd out the
+// block's loads; in fp32 (540 MB) 114 us, 4.7 TB/s, of 2 rows a key head on half as many
+// 85, of 4 on a quarter 41.  Past 4 rows the registers of the rows' accumulators crowd out the
 // loads in flight (8 rows, 2 key heads of 131072 keys: 63 us).
 //
 // The work is cut as in the tensor-core kernels (cross_sched.cuh): CTAs of 8 warps
@@ -217,10 +218,10 @@ cross_few_kernel(const FArgs a) {
 // product's operand as they lie, and transposed 8 x 8 (movmatrix) the value product's.
 // The weights go back as two bf16 numbers, high and low part; the denominator is the sum of
 // both.  A warp has 16 keys of the next block in flight while it works on one.  2 key heads
-// of 131072 keys, 8 rows (67 MB): 12.1 us, 5.5 TB/s, and 6 for the join of 296 pieces; on the
+// of 131072 keys, 8 rows (67 MB, which stay in L2): 12.1 us, and 6 for the join of 296 pieces; on the
 // 128-row tiles 15.5 and 4.7 with the weights as precise.  One CTA of 16 warps per SM: 18 us.
-// 4 rows on 64 x 4 key heads of 1500 keys (98 MB), with the join: 35 us on the CUDA cores, 27
-// so; 1 and 2 rows are 5% slower so.
+// 4 rows on 64 x 4 key heads of 1500 keys (98 MB, in L2 too), with the join: 35 us on the CUDA
+// cores, 24 so; 1 and 2 rows are 5% slower so.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));

@@ -30,6 +30,10 @@
 // rounding.  (8192 queries, 16384 keys, 8 heads: 295 us with the rounded weights summed
 // by the warps, 265 us with the unrounded ones, 258 us this way.)
 //
+// Times in this file compare variants in short bursts, 20 launches of a captured graph,
+// at the step that they were measured.  As it stands that prompt takes 243 us so, and 273
+// to 289 us in an unbroken run, where the power cap lowers the clock.
+//
 // Schedule.  The work is a line of units, one per (128-row tile, column block),
 // sequence by sequence; every CTA of the persistent grid takes an equal stretch
 // of it (cross_sched.cuh), whatever the lengths, and walks the stretch item by

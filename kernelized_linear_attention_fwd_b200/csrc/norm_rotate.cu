@@ -338,10 +338,10 @@ constexpr int kNormRing = kNormWarps * kNormStages * kSetBytes;
 // copied itself (so nothing but its own copies is waited for); the gradient with sets of
 // twice the rows and the ring of four sets: no faster.  Loads into registers, one set at
 // a time, took 95 us for 65536 tokens of 16 + 16 heads of 64 (537 MB; so 87 us, 6.2 TB/s), and
-// 72 us for the gradient of 32768 tokens of 16 + 4 heads (252 MB; so 61 us, 4.1 TB/s: its
-// arithmetic keeps two thirds of the issue slots busy).  The arithmetic is packed (fp32
-// pairs) and the forward's gains are folded into the angles once per token and tensor
-// (139 us without either).
+// 72 us for the gradient of 32768 tokens of 16 + 4 heads (252 MB; so 60 us, 4.2 TB/s: its
+// arithmetic keeps two thirds of the issue slots busy; in fp32, 503 MB, 87 us, 5.8 TB/s).
+// The arithmetic is packed (fp32 pairs) and the forward's gains are folded into the angles
+// once per token and tensor (139 us without either).
 
 template <typename T, int D, bool INTER, bool BWD>
 __global__ void __launch_bounds__(32 * kNormWarps, norm_per_sm(BWD))
