@@ -472,7 +472,7 @@ kata_status kata_qk_norm_rotate_backward(
  * (the weights of this file's head with the causal mask replaced by a length;
  * the convex output gate of summary 2.1 holds as before).  Weights and their
  * sums are fp32 numbers: l_t below 2^-126, the smallest normal one, counts as 0
- * (here and in the gradient), and past 2^128 y_t is not a number.
+ * (here and in the gradient), and one past 2^128 has no defined y_t.
  *
  *   q      [B, H, Tq, d] dtype     out  [B, H, Tq, d] dtype
  *   k, v   [B, Hkv, Tk, d] dtype; Hkv divides H, query head h uses key head

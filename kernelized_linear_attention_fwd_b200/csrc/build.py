@@ -9,6 +9,7 @@ missing, or the compiler fails, it is left out and the binding works without it.
 Cross-compiles without a GPU.  `--verbose` adds -Xptxas -v (registers, spills, shared
 memory per kernel).
 """
+import contextlib
 import glob
 import importlib.util
 import os
@@ -92,16 +93,18 @@ def build_calls(force=False):
     built for other declarations, are removed, whatever torch and Python they are for."""
     deps = [CALLS_SRC, os.path.join(ROOT, "include", "kata.h"), __file__]
     for f in glob.glob(os.path.join(PKG, "_calls*.so")):
-        if any(os.path.getmtime(d) > os.path.getmtime(f) for d in deps):
-            os.remove(f)
+        with contextlib.suppress(FileNotFoundError):  # another process builds too
+            if any(os.path.getmtime(d) > os.path.getmtime(f) for d in deps):
+                os.remove(f)
     out = calls_out()
     if out and os.path.exists(out) and not force:
         return lambda: None
 
     def without(why):
         print(why + ": built without " + os.path.basename(out or "_calls.so"))
-        if out and os.path.exists(out):
-            os.remove(out)
+        if out:
+            with contextlib.suppress(FileNotFoundError):
+                os.remove(out)
 
     tmp = "%s.tmp%d" % (out, os.getpid())
     cmd = calls_command(tmp) if out else None

@@ -86,6 +86,16 @@ def test_the_library_is_built_where_the_short_cut_fails(elsewhere, monkeypatch, 
     assert len(ran) == 1 and names(folder) == ["libkata.so"]
 
 
+def test_another_process_removes_the_same_old_file(elsewhere, monkeypatch):
+    folder, _ = elsewhere
+    monkeypatch.setattr(kbuild.glob, "glob", lambda pattern: [str(folder / "_calls-gone.so")])
+    monkeypatch.setattr(kbuild, "sources", lambda: [])
+    monkeypatch.setattr(kbuild, "headers", lambda: [])
+    monkeypatch.setattr(kbuild, "calls_command", lambda out: ["false"])
+    kbuild.build(force=True)
+    assert names(folder) == ["libkata.so"]
+
+
 def test_a_failing_library_build_leaves_no_compiler_behind(elsewhere, monkeypatch):
     folder, _ = elsewhere
     monkeypatch.setattr(kbuild, "calls_command", lambda out: ["sh", "-c", "sleep 0.3; : > " + out])
