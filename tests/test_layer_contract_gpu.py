@@ -131,3 +131,25 @@ def test_a_pair_of_calls_in_an_autograd_function():
             bounds = O.cross_bounds(q.detach(), k.detach(), v.detach(), torch.float32, n, dout=up)
             for a, r, b in zip(got, ref, bounds):
                 assert O.worst(a / 2, r, b) <= 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,Hk,Tq,Tk", [(2, 2, 1, 300), (8, 2, 1, 5000), (6, 3, 11, 400), (4, 2, 33, 500), (4, 2, 300, 517)])
+def test_a_bad_query_stays_in_its_row(dtype, H, Hk, Tq, Tk):
+    # a query that is not finite, or overflows: the other rows of its tile, their gradients and
+    # the other key heads' keep their bits
+    q, k, v, g = make(2, H, Hk, Tq, Tk, 32, dtype, seed=Tk)
+    n = lens(Tk, Tk // 2)
+    a = forward(q, k, v, n)
+    ga = K.kata_cross_backward(g, q, k, v, a[1], a[2], key_lengths=n)
+    keep = torch.ones(2, H, Tq, dtype=torch.bool, device="cuda")
+    keep[:, 0, Tq // 2] = False
+    for value in (float("nan"), float("inf"), torch.finfo(q.dtype).max):
+        bad = q.clone()
+        bad[:, 0, Tq // 2, 1] = value
+        b = forward(bad, k, v, n)
+        gb = K.kata_cross_backward(g, bad, k, v, b[1], b[2], key_lengths=n)
+        for x, y in zip(a + ga[:1], b + gb[:1]):
+            assert torch.equal(x[keep], y[keep])
+        for x, y in zip(ga[1:], gb[1:]):
+            assert torch.equal(x[:, 1:], y[:, 1:])
